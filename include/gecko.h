@@ -345,6 +345,135 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
                          float beta1, float beta2, float eps, int dtype, void* stream);
 
 /*
+ * The layer steps around the path (below): the gated recurrence, the
+ * projection, and the queries and keys from the shared representation, each
+ * with its gradients.  Unlike the calls above they take their working memory
+ * from the caller: gecko_*_workspace() writes the bytes that a call of these
+ * sizes needs (0: none, workspace may be NULL); a workspace is 16-byte
+ * aligned device memory, needs no initial contents, and may be reused once
+ * the call's work on its stream is done.  So calls on different streams, or
+ * captured into different CUDA graphs, share nothing as long as they are given
+ * different workspaces.  Every pointer is 16-byte aligned device memory of
+ * the current device (reset: any alignment) and every tensor is contiguous.
+ * Outputs are fully overwritten and must not alias inputs or each other
+ * except where stated.  Execution is asynchronous on `stream`; argument errors
+ * are found on the host before anything is launched or written.  Returns
+ * GECKO_OK, GECKO_ERR_ARG (also a workspace that is too small),
+ * GECKO_ERR_SHAPE, GECKO_ERR_ALIGN or GECKO_ERR_CUDA.
+ */
+
+/*
+ * gecko_gated_scan_forward - gated linear recurrence, the companion of CEMA
+ * whose gates depend on the input (CEMA's alpha, delta and theta are fixed
+ * parameters of the layer).  Per batch b and feature d:
+ *   a_t = exp(log_a_t), h_t = a_t h_{t-1} + x_t, y_t = h_t
+ * held in fp32.  A gate of log_a = -inf (or low enough that exp is 0), or a
+ * document start at token t (reset), drops the first term: h_t = x_t.
+ *
+ *   x, log_a, y : [B, L, D] dtype `dtype`; y may equal x.
+ *   reset       : [B, L] uint8 or NULL; non-zero = a document starts there.
+ *   state_in    : [B, D] fp32 h_{-1}, or NULL for zero.
+ *   state_out   : [B, D] fp32 receives h_{L-1}, or NULL; may equal state_in.
+ *                 Chaining state_out into state_in runs a long sequence in
+ *                 segments, down to one token at a time.
+ *   chunk_state : [B, ceil(L / GECKO_SCAN_CHUNK), D] fp32, or NULL: receives
+ *                 the state entering each chunk of GECKO_SCAN_CHUNK tokens,
+ *                 all that the backward keeps of the forward (chunk-boundary
+ *                 storage and rematerialisation as in the paperlayer.ai
+ *                 summary, Appendix B.1).
+ *   Requires D % 8 == 0, B <= 65535, L <= 65535 * GECKO_SCAN_CHUNK,
+ *   D <= 2^24.
+ *
+ * gecko_gated_scan_backward - its gradients:
+ *   dh_t = dy_t + a_{t+1} dh_{t+1}  (dh_{L-1} = dy_{L-1} + dstate_out),
+ *   dx_t = dh_t,  dlog_a_t = dh_t a_t h_{t-1},  dstate_in = a_0 dh_0
+ * (0 in place of the products where the forward dropped the term).
+ *   dy, dx, dlog_a : [B, L, D] dtype; dx may equal dy.
+ *   chunk_state    : as the forward wrote it.
+ *   dstate_out     : [B, D] fp32 gradient of state_out, or NULL for zero.
+ *   dstate_in      : [B, D] fp32, or NULL; may equal dstate_out.
+ */
+#define GECKO_SCAN_CHUNK 256
+int gecko_gated_scan_workspace(int64_t B, int64_t L, int64_t D, int dtype, int backward, int64_t* bytes);
+int gecko_gated_scan_forward(const void* x, const void* log_a, void* y, const uint8_t* reset, const float* state_in,
+                             float* state_out, float* chunk_state, int64_t B, int64_t L, int64_t D, int dtype,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+int gecko_gated_scan_backward(const void* x, const void* log_a, const void* dy, const uint8_t* reset,
+                              const float* chunk_state, const float* dstate_out, void* dx, void* dlog_a,
+                              float* dstate_in, int64_t B, int64_t L, int64_t D, int dtype, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/*
+ * gecko_qk_forward - the inputs q, k, q_m, k_m of the SCA + AWM path from the
+ * shared representation z = X W_z + b_z (Gecko digest, method step details,
+ * steps 2-4).  Per batch b, token t and head h, with z_bth its d features:
+ *   z' = z_bth / max(|z_bth|_2, eps)
+ *   p_i = scale_i (.) z' + shift_i      for i = q, k, q_m, k_m
+ * and q and k are then turned by the token's position (the pages print no
+ * rotation; rot_dim = 0 gives their form): of each head's first rot_dim
+ * features the pairs (a, b) become (a cos w - b sin w, b cos w + a sin w), with
+ * w = pos * rot_base^(-2 i / rot_dim) for pair i, the pairs being features
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved is not 0.  Angles are
+ * formed in fp64.  The sum of squares is taken in fp32: it must stay finite.
+ *
+ *   z            : [B, T, H * d] dtype `dtype`.
+ *   scale, shift : [4, H, d] fp32 (q, k, q_m, k_m).
+ *   pos          : [B, T] int64 positions, or NULL for pos0 + t.
+ *   q, k, qm, km : [B, H, T, d] dtype.
+ *   Requires d in {64, 128}, rot_dim a multiple of 16 with 0 <= rot_dim <= d,
+ *   rot_base >= 1 (read if rot_dim > 0), eps > 0, H <= 65535,
+ *   B, T < 2^31, B * T < 2^35.
+ *
+ * gecko_qk_backward - its gradients for dq, dk, dqm, dkm [B, H, T, d]:
+ * dz [B, T, H * d] dtype; dscale, dshift [4, H, d] fp32 (summed in a fixed
+ * order).  z and scale as in the forward.
+ */
+int gecko_qk_forward(const void* z, const float* scale, const float* shift, const int64_t* pos, void* q, void* k,
+                     void* qm, void* km, int64_t B, int64_t T, int64_t H, int64_t d, float eps, int64_t pos0,
+                     int64_t rot_dim, double rot_base, int interleaved, int dtype, void* stream);
+int gecko_qk_workspace(int64_t B, int64_t T, int64_t H, int64_t d, int64_t* bytes);   /* of the backward */
+int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, const void* dq, const void* dk,
+                      const void* dqm, const void* dkm, void* dz, float* dscale, float* dshift, int64_t B,
+                      int64_t T, int64_t H, int64_t d, float eps, int64_t pos0, int64_t rot_dim, double rot_base,
+                      int interleaved, int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * gecko_linear_forward - a projection with its epilogue (Gecko digest, method
+ * step details: Z = X W_z + b_z in step 2, V = SiLU(X W_v + b_v) in step 3):
+ *   u = x w^T + bias,  y = f(u) + residual
+ * with f the identity, SiLU u / (1 + e^-u) or GELU u Phi(u) (Phi the normal
+ * distribution function).  fp32 accumulation; one rounding of y.
+ *
+ *   x        : [B, T, K] dtype `dtype`.
+ *   w        : [N, K] dtype.
+ *   bias     : [N] fp32 or NULL.
+ *   y        : [B, T, N] dtype if H = 0, else [B, H, T, N / H]: the path's
+ *              layout, so v comes out of its projection ready for SCA.
+ *   residual : in y's layout and dtype, or NULL.  pre: NULL, or in y's
+ *              layout: receives u, which the backward of an activation needs.
+ *   Requires N % 8 == 0, K % 8 == 0, (N / H) % 8 == 0 if H > 0,
+ *   B * T <= 2^31 - 256, N and K <= 2^20.
+ *
+ * gecko_linear_backward - the gradients for dy (y's layout): with
+ * du = dy f'(u), rounded to dtype once as the operand of the products,
+ *   dx = du w [B, T, K],  dw = du^T x [N, K]  (dtype),
+ *   db [N] fp32 = column sums of the unrounded du.
+ * Any of dx, dw, db may be NULL (not wanted), but not all.  pre may be NULL
+ * for the identity.  The gradient of residual is dy.
+ */
+#define GECKO_ACT_NONE 0
+#define GECKO_ACT_SILU 1
+#define GECKO_ACT_GELU 2
+int gecko_linear_workspace(int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype, int backward,
+                           int64_t* bytes);
+int gecko_linear_forward(const void* x, const void* w, const float* bias, const void* residual, void* y, void* pre,
+                         int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+int gecko_linear_backward(const void* x, const void* w, const void* dy, const void* pre, void* dx, void* dw,
+                          float* db, int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * Context parallelism: one sequence split into P consecutive segments of
  * T tokens each (one per rank, T % c == 0), run so that the outputs equal a
  * single call over the whole sequence (up to rounding).  The AWM carry is

@@ -72,8 +72,8 @@ Workspace carve_workspace(void* base, int64_t BH, int64_t T, int64_t c, int64_t 
 }
 
 namespace {
-
 thread_local std::string t_err;
+}
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -84,6 +84,8 @@ int fail(int code, const char* fmt, ...) {
   t_err = buf;
   return code;
 }
+
+namespace {
 
 struct DeviceState {
   void* ws = nullptr;
@@ -127,6 +129,20 @@ int device_state(int dev, DeviceState** out) {
   *out = &ds;
   return GECKO_OK;
 }
+
+}  // namespace
+
+int device_status_word(int** word) {
+  int dev = 0, rc;
+  if ((rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice"))) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(dev, &ds))) return rc;
+  *word = ds->status;
+  return GECKO_OK;
+}
+
+namespace {
 
 constexpr int64_t kMaxGridYZ = 65535;
 

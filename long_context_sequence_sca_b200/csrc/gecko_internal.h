@@ -10,6 +10,12 @@ namespace gecko {
 constexpr int kF32 = 0;
 constexpr int kBF16 = 1;
 
+// Set this thread's error message and return `code`.
+int fail(int code, const char* fmt, ...);
+// Device address of the current device's status word (bounded waits that ran
+// out); returns a gecko status.
+int device_status_word(int** word);
+
 // One validated forward call.
 struct Problem {
   const void *q, *k, *v, *qm, *km;
@@ -194,5 +200,93 @@ struct NormWorkspace {
 size_t tdnorm_workspace_bytes(int64_t B, int64_t L, int64_t G);
 NormWorkspace carve_tdnorm_workspace(void* base, int64_t B, int64_t L, int64_t G);
 cudaError_t launch_tdnorm(const NormProblem& p, const NormWorkspace& w, cudaStream_t st);
+
+// --------------------------------------------------- gated recurrence --
+
+// Tokens per chunk of the gated scan: the spacing of the states that the
+// forward keeps for the backward.
+constexpr int kScanChunk = 256;
+inline int64_t scan_chunks(int64_t L) { return (L + kScanChunk - 1) / kScanChunk; }
+
+// One validated call: x, log_a [B, L, D] (dtype); reset [B, L] uint8 or null.
+// Forward: y [B, L, D]; state_in / state_out [B, D] fp32 or null; chunk_state
+// [B, scan_chunks(L), D] fp32 or null.  Backward: dy, dx, dlog_a [B, L, D];
+// chunk_state as the forward wrote it; dstate_out / dstate_in [B, D] or null.
+struct ScanProblem {
+  const void *x, *log_a;
+  const uint8_t* reset;
+  void* y;
+  const float* state_in;
+  float* state_out;
+  float* chunk_state;
+  const void* dy;
+  const float* dstate_out;
+  void *dx, *dlog_a;
+  float* dstate_in;
+  int64_t B, L, D;
+  int dtype;
+  void* ws;
+  int* status;
+};
+
+size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype, bool backward);
+cudaError_t launch_scan(const ScanProblem& p, cudaStream_t st);
+cudaError_t launch_scan_bwd(const ScanProblem& p, cudaStream_t st);
+
+// ------------------------------------------- queries and keys from z --
+
+constexpr int kMaxRotPairs = 64;
+
+// One validated call: z, dz [B, T, H * d]; the four streams i = q, k, q_m,
+// k_m as out[i] (forward) or dout[i] (backward) [B, H, T, d]; scale, shift,
+// dscale, dshift [4, H, d] fp32; pos [B, T] int64 or null (pos0 + t).
+// rate[i]: revolutions per position of rotated pair i (rot_dim / 2 of them).
+struct QkProblem {
+  const void* z;
+  const float *scale, *shift;
+  const int64_t* pos;
+  void* out[4];
+  const void* dout[4];
+  void* dz;
+  float *dscale, *dshift;
+  int64_t B, T, H, d;
+  float eps;
+  int64_t pos0;
+  int rot_dim;
+  bool interleaved;
+  int dtype;
+  void* ws;
+  double rate[kMaxRotPairs];
+};
+
+size_t qk_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d);   // backward
+cudaError_t launch_qk(const QkProblem& p, cudaStream_t st);
+cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
+
+// ---------------------------------------------------------- projection --
+
+constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
+
+// One validated call.  x [M, K], w [N, K], M = B * T; y, pre, residual, dy
+// [M, N], or [B, H, T, N / H] where H > 0; dx [M, K], dw [N, K], db [N] fp32.
+struct LinearProblem {
+  const void *x, *w;
+  const float* bias;
+  const void* residual;
+  void *y, *pre;
+  const void* dy;
+  void *dx, *dw;
+  float* db;
+  int64_t B, T, N, K, H;
+  int act;
+  int dtype;
+  void* ws;
+  int* status;
+  int64_t M() const { return B * T; }
+};
+
+size_t linear_workspace_bytes(const LinearProblem& p, bool backward);
+cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st);
+cudaError_t launch_linear_bwd(const LinearProblem& p, cudaStream_t st);
 
 }  // namespace gecko

@@ -1,0 +1,212 @@
+// Projection y = f(x w^T + bias) + residual and its gradients:
+//   u = x w^T + bias,  du = dy (.) f'(u),
+//   dx = du w,  dw = du^T x,  db = column sums of du.
+// CUDA-core kernels for every type.
+#include "common.cuh"
+#include "gecko_internal.h"
+#include "linear.cuh"
+
+namespace gecko {
+namespace {
+
+// ------------------------------------------------------ CUDA-core product --
+
+// C[m, n] = sum_k A(m, k) B(n, k) with A(m, k) = A[m am + k ak] and likewise
+// B: 64 x 64 tiles, 4 x 4 results per thread, fp32 FMA.
+constexpr int kSimtTile = 64, kSimtK = 16;
+
+template <typename T, class Epilogue>
+__global__ void __launch_bounds__(256) simt_gemm_kernel(const T* A, int64_t am, int64_t ak, const T* B, int64_t bn,
+                                                        int64_t bk, int64_t M, int64_t N, int64_t K, Epilogue ep) {
+  __shared__ float As[kSimtK][kSimtTile + 4], Bs[kSimtK][kSimtTile + 4];
+  const int64_t m0 = (int64_t)blockIdx.x * kSimtTile, n0 = (int64_t)blockIdx.y * kSimtTile;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float acc[4][4] = {};
+  for (int64_t k0 = 0; k0 < K; k0 += kSimtK) {
+    for (int i = threadIdx.x; i < kSimtTile * kSimtK; i += 256) {
+      // consecutive threads along the operand's contiguous dimension
+      const int ra = ak == 1 ? i / kSimtK : i % kSimtTile, ka = ak == 1 ? i % kSimtK : i / kSimtTile;
+      As[ka][ra] = m0 + ra < M && k0 + ka < K ? to_f32(A[(m0 + ra) * am + (k0 + ka) * ak]) : 0.f;
+      const int rb = bk == 1 ? i / kSimtK : i % kSimtTile, kb = bk == 1 ? i % kSimtK : i / kSimtTile;
+      Bs[kb][rb] = n0 + rb < N && k0 + kb < K ? to_f32(B[(n0 + rb) * bn + (k0 + kb) * bk]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSimtK; ++k) {
+      float a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = As[k][ty * 4 + i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = Bs[k][tx * 4 + j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+      if (m < M && n < N) ep(m, n, acc[i][j]);
+    }
+}
+
+// u -> y (and the kept u)
+template <typename T>
+struct ForwardOut {
+  const float* bias;
+  const T* residual;
+  T *y, *pre;
+  OutLayout lay;
+  int act;
+  __device__ void operator()(int64_t m, int64_t n, float u) const {
+    if (bias) u += bias[n];
+    const int64_t at = lay.at(m, n);
+    if (pre) pre[at] = from_f32<T>(u);
+    float v = activate(u, act);
+    if (residual) v += to_f32(residual[at]);
+    y[at] = from_f32<T>(v);
+  }
+};
+
+template <typename T>
+struct PlainOut {
+  T* c;
+  int64_t ld;
+  __device__ void operator()(int64_t m, int64_t n, float v) const { c[m * ld + n] = from_f32<T>(v); }
+};
+
+template <typename T, class Epilogue>
+void simt_gemm(const void* A, int64_t am, int64_t ak, const void* B, int64_t bn, int64_t bk, int64_t M, int64_t N,
+               int64_t K, const Epilogue& ep, cudaStream_t st) {
+  const dim3 grid((unsigned)((M + kSimtTile - 1) / kSimtTile), (unsigned)((N + kSimtTile - 1) / kSimtTile));
+  simt_gemm_kernel<T, Epilogue><<<grid, 256, 0, st>>>(static_cast<const T*>(A), am, ak, static_cast<const T*>(B), bn,
+                                                      bk, M, N, K, ep);
+}
+
+// ----------------------------------------------------- gradient of u, db --
+
+constexpr int kDuCols = 256;     // columns per block: 32 threads x 8
+constexpr int kDuRowsPar = 8;    // rows in flight per block
+
+// du = dy f'(u), [M, N] row-major in the tensors' type (one rounding, the
+// operand type of the two products that follow); the column sums of the
+// unrounded values go to part [gridDim.y, N].
+template <typename T>
+__global__ void __launch_bounds__(256) linear_du_kernel(const T* dy, const T* pre, T* du, float* part, OutLayout lay,
+                                                        int64_t M, int64_t N, int64_t rows, int act) {
+  __shared__ float red[kDuRowsPar][kDuCols];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * kDuCols + cx * 8;
+  const int64_t m1 = min(M, ((int64_t)blockIdx.y + 1) * rows);
+  float acc[8] = {};
+  if (n < N)
+    for (int64_t m = (int64_t)blockIdx.y * rows + ry; m < m1; m += kDuRowsPar) {
+      const int64_t at = lay.at(m, n);
+      float g[8], u[8];
+      load_f8(dy + at, g);
+      if (act != kActNone) {
+        load_f8(pre + at, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] *= act_slope(u[i], act);
+      }
+      if (du) store_f8(du + m * N + n, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += g[i];
+    }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[ry][cx * 8 + i] = acc[i];
+  __syncthreads();
+  const int64_t col = (int64_t)blockIdx.x * kDuCols + threadIdx.x;
+  if (col < N) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDuRowsPar; ++i) s += red[i][threadIdx.x];
+    part[blockIdx.y * N + col] = s;
+  }
+}
+
+// db: the partial column sums in a fixed order.
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int rows, int64_t N, float* db) {
+  __shared__ float red[8][32];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + cx;
+  float acc = 0.f;
+  if (col < N)
+    for (int r = ry; r < rows; r += 8) acc += part[r * N + col];
+  red[ry][cx] = acc;
+  __syncthreads();
+  if (ry == 0 && col < N) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) acc += red[i][cx];
+    db[col] = acc;
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Blocks of rows of the du pass.
+int64_t du_row_blocks(int64_t M, int64_t N) {
+  const int64_t cols = (N + kDuCols - 1) / kDuCols;
+  int64_t blocks = (148 * 8 + cols - 1) / cols;
+  const int64_t most = (M + 4 * kDuRowsPar - 1) / (4 * kDuRowsPar);
+  return blocks < most ? blocks : most;
+}
+
+// Whether dy itself is du, laid out as the products need it.
+bool dy_is_du(const LinearProblem& p) { return p.act == kActNone && p.H == 0; }
+
+template <typename T>
+cudaError_t forward_simt(const LinearProblem& p, cudaStream_t st) {
+  ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
+                   OutLayout(p), p.act};
+  simt_gemm<T>(p.x, p.K, 1, p.w, p.K, 1, p.M(), p.N, p.K, ep, st);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
+  const int64_t M = p.M();
+  char* ws = static_cast<char*>(p.ws);
+  const bool alias = dy_is_du(p);
+  T* du = alias ? nullptr : reinterpret_cast<T*>(ws);
+  float* part = reinterpret_cast<float*>(ws + (alias ? 0 : up256(sizeof(T) * M * p.N)));
+  const bool products = p.dx || p.dw;
+  if (p.db || (!alias && products)) {
+    const int64_t blocks = du_row_blocks(M, p.N), rows = (M + blocks - 1) / blocks;
+    const dim3 grid((unsigned)((p.N + kDuCols - 1) / kDuCols), (unsigned)blocks);
+    linear_du_kernel<T><<<grid, 256, 0, st>>>(static_cast<const T*>(p.dy), static_cast<const T*>(p.pre),
+                                              products ? du : nullptr, p.db ? part : nullptr, OutLayout(p), M, p.N,
+                                              rows, p.act);
+    if (p.db)
+      linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
+  }
+  const void* g = alias ? p.dy : du;
+  if (p.dx)
+    simt_gemm<T>(g, p.N, 1, p.w, 1, p.K, M, p.K, p.N, PlainOut<T>{static_cast<T*>(p.dx), p.K}, st);
+  if (p.dw)
+    simt_gemm<T>(g, 1, p.N, p.x, 1, p.K, p.N, p.K, M, PlainOut<T>{static_cast<T*>(p.dw), p.K}, st);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t linear_workspace_bytes(const LinearProblem& p, bool backward) {
+  if (!backward) return 0;
+  const size_t e = p.dtype == kBF16 ? 2 : 4;
+  return (dy_is_du(p) ? 0 : up256(e * p.M() * p.N)) + up256(sizeof(float) * du_row_blocks(p.M(), p.N) * p.N);
+}
+
+cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st) {
+  return p.dtype == kBF16 ? forward_simt<__nv_bfloat16>(p, st) : forward_simt<float>(p, st);
+}
+
+cudaError_t launch_linear_bwd(const LinearProblem& p, cudaStream_t st) {
+  return p.dtype == kBF16 ? backward_impl<__nv_bfloat16>(p, st) : backward_impl<float>(p, st);
+}
+
+}  // namespace gecko

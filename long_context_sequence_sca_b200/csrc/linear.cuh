@@ -1,0 +1,65 @@
+// Pieces shared by the projection's kernels: the activations, 8-element
+// loads and stores, and the output layouts.
+#pragma once
+
+#include "common.cuh"
+#include "gecko_internal.h"
+
+namespace gecko {
+
+// f(u): SiLU u / (1 + e^-u); GELU u Phi(u), with Phi(u) = erfc(-u / sqrt 2) / 2
+// (no cancellation for negative u).
+__device__ __forceinline__ float activate(float u, int act) {
+  if (act == kActSilu) return u / (1.f + __expf(-u));
+  if (act == kActGelu) return 0.5f * u * erfcf(-0.7071067811865476f * u);
+  return u;
+}
+
+// f'(u): SiLU s (1 + u (1 - s)), s = 1 / (1 + e^-u); GELU Phi(u) + u phi(u).
+__device__ __forceinline__ float act_slope(float u, int act) {
+  if (act == kActSilu) {
+    const float s = 1.f / (1.f + __expf(-u));
+    return s * fmaf(u, 1.f - s, 1.f);
+  }
+  if (act == kActGelu)
+    return 0.5f * erfcf(-0.7071067811865476f * u) + u * 0.3989422804014327f * __expf(-0.5f * u * u);
+  return 1.f;
+}
+
+__device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load_f8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store_f8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_f8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                            pack_bf16x2(v[6], v[7]));
+}
+
+// Where element (m, n) of y, pre, residual and dy lies: [M, N] row-major, or
+// [B, H, T, N / H] (m = b T + t, n = h N / H + j).
+struct OutLayout {
+  int64_t N, T, H;
+  int hd;
+  explicit OutLayout(const LinearProblem& p) : N(p.N), T(p.T), H(p.H), hd(p.H ? (int)(p.N / p.H) : 1) {}
+  __device__ __forceinline__ int64_t at(int64_t m, int64_t n) const {
+    if (H == 0) return m * N + n;
+    const int64_t b = m / T, t = m - b * T;
+    const int h = (int)n / hd, j = (int)n - h * hd;
+    return ((b * H + h) * T + t) * hd + j;
+  }
+};
+
+}  // namespace gecko

@@ -23,6 +23,15 @@ EXPORTS = (
     "gecko_awm_state",
     "gecko_cema_forward",
     "gecko_tdnorm_forward",
+    "gecko_gated_scan_workspace",
+    "gecko_gated_scan_forward",
+    "gecko_gated_scan_backward",
+    "gecko_qk_forward",
+    "gecko_qk_workspace",
+    "gecko_qk_backward",
+    "gecko_linear_workspace",
+    "gecko_linear_forward",
+    "gecko_linear_backward",
     "gecko_awm_segment_logsum",
     "gecko_awm_segment_maps",
     "gecko_awm_cp_logz",
@@ -84,6 +93,20 @@ def load() -> ctypes.CDLL:
     lib.gecko_tdnorm_forward.argtypes = [vp] * 4 + [i64] * 4 + [f32, f32, f32, ctypes.c_int, vp]
     lib.gecko_tdnorm_forward.restype = ctypes.c_int
     ci = ctypes.c_int
+    f64, out = ctypes.c_double, ctypes.POINTER(ctypes.c_int64)
+    rot = [f32, i64, i64, f64, ci]
+    for name, args in (
+            ("gated_scan_workspace", [i64] * 3 + [ci, ci, out]),
+            ("gated_scan_forward", [vp] * 7 + [i64] * 3 + [ci, vp, i64, vp]),
+            ("gated_scan_backward", [vp] * 9 + [i64] * 3 + [ci, vp, i64, vp]),
+            ("qk_forward", [vp] * 8 + [i64] * 4 + rot + [ci, vp]),
+            ("qk_workspace", [i64] * 4 + [out]),
+            ("qk_backward", [vp] * 10 + [i64] * 4 + rot + [ci, vp, i64, vp]),
+            ("linear_workspace", [i64] * 5 + [ci, ci, ci, out]),
+            ("linear_forward", [vp] * 6 + [i64] * 5 + [ci, ci, vp, i64, vp]),
+            ("linear_backward", [vp] * 7 + [i64] * 5 + [ci, ci, vp, i64, vp])):
+        fn = getattr(lib, "gecko_" + name)
+        fn.argtypes, fn.restype = args, ci
     lib.gecko_awm_segment_logsum.argtypes = [vp, vp] + [i64] * 5 + [ci, vp]
     lib.gecko_awm_segment_logsum.restype = ci
     lib.gecko_awm_segment_maps.argtypes = [vp] * 4 + [i64] * 5 + [ci, vp]
@@ -168,6 +191,57 @@ def gecko_cema_forward(x, y, alpha, delta, theta, beta, eta, reset, state_in, st
 def gecko_tdnorm_forward(x, y, gamma, bias, B, L, D, G, beta1, beta2, eps, dtype, stream) -> int:
     """Direct call of the timestep-normalisation entry point with integer pointers."""
     return load().gecko_tdnorm_forward(x, y, gamma, bias, B, L, D, G, beta1, beta2, eps, dtype, stream)
+
+
+def gecko_gated_scan_workspace(B, L, D, dtype, backward, bytes_out) -> int:
+    return load().gecko_gated_scan_workspace(B, L, D, dtype, backward, bytes_out)
+
+
+def gecko_gated_scan_forward(x, log_a, y, reset, state_in, state_out, chunk_state, B, L, D, dtype, workspace,
+                             workspace_bytes, stream) -> int:
+    """Direct call of the gated recurrence with integer pointers (0 = NULL)."""
+    return load().gecko_gated_scan_forward(x, log_a, y, reset, state_in, state_out, chunk_state, B, L, D, dtype,
+                                           workspace, workspace_bytes, stream)
+
+
+def gecko_gated_scan_backward(x, log_a, dy, reset, chunk_state, dstate_out, dx, dlog_a, dstate_in, B, L, D, dtype,
+                              workspace, workspace_bytes, stream) -> int:
+    return load().gecko_gated_scan_backward(x, log_a, dy, reset, chunk_state, dstate_out, dx, dlog_a, dstate_in,
+                                            B, L, D, dtype, workspace, workspace_bytes, stream)
+
+
+def gecko_qk_forward(z, scale, shift, pos, q, k, qm, km, B, T, H, d, eps, pos0, rot_dim, rot_base, interleaved,
+                     dtype, stream) -> int:
+    """Direct call of the query/key step with integer pointers (0 = NULL)."""
+    return load().gecko_qk_forward(z, scale, shift, pos, q, k, qm, km, B, T, H, d, eps, pos0, rot_dim, rot_base,
+                                   interleaved, dtype, stream)
+
+
+def gecko_qk_workspace(B, T, H, d, bytes_out) -> int:
+    return load().gecko_qk_workspace(B, T, H, d, bytes_out)
+
+
+def gecko_qk_backward(z, scale, pos, dq, dk, dqm, dkm, dz, dscale, dshift, B, T, H, d, eps, pos0, rot_dim, rot_base,
+                      interleaved, dtype, workspace, workspace_bytes, stream) -> int:
+    return load().gecko_qk_backward(z, scale, pos, dq, dk, dqm, dkm, dz, dscale, dshift, B, T, H, d, eps, pos0,
+                                    rot_dim, rot_base, interleaved, dtype, workspace, workspace_bytes, stream)
+
+
+def gecko_linear_workspace(B, T, N, K, H, act, dtype, backward, bytes_out) -> int:
+    return load().gecko_linear_workspace(B, T, N, K, H, act, dtype, backward, bytes_out)
+
+
+def gecko_linear_forward(x, w, bias, residual, y, pre, B, T, N, K, H, act, dtype, workspace, workspace_bytes,
+                         stream) -> int:
+    """Direct call of the projection with integer pointers (0 = NULL)."""
+    return load().gecko_linear_forward(x, w, bias, residual, y, pre, B, T, N, K, H, act, dtype, workspace,
+                                       workspace_bytes, stream)
+
+
+def gecko_linear_backward(x, w, dy, pre, dx, dw, db, B, T, N, K, H, act, dtype, workspace, workspace_bytes,
+                          stream) -> int:
+    return load().gecko_linear_backward(x, w, dy, pre, dx, dw, db, B, T, N, K, H, act, dtype, workspace,
+                                        workspace_bytes, stream)
 
 
 def gecko_awm_segment_logsum(km, lsum_out, B, H, T, c, d, dtype, stream) -> int:
@@ -449,6 +523,285 @@ def tdnorm_forward(x, gamma, bias, G: int, beta1: float, beta2: float, eps: floa
                                   beta1, beta2, eps, _DT[x.dtype], _stream_handle(stream))
     _check(rc)
     return y
+
+
+# -------------------------------------------- layer steps around the path --
+
+SCAN_CHUNK = 256
+ACTS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _tensor(t, name, shape, dtype, device):
+    """Check one argument; None stays None."""
+    if t is not None and not (isinstance(t, torch.Tensor) and t.is_contiguous() and tuple(t.shape) == shape
+                              and t.dtype == dtype and t.device == device):
+        raise ValueError(f"{name} must be a contiguous {shape} {dtype} tensor on {device}")
+    return t
+
+
+def _main(t, name, ndim=3):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() == ndim and t.dtype in _DT):
+        raise ValueError(f"{name} must be a contiguous {ndim}-dimensional float32 or bfloat16 CUDA tensor")
+    return t
+
+
+def _required(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+class _on:
+    """The tensors' device and the call's stream as torch's current ones, so
+    that outputs and workspaces are allocated for the stream that uses them."""
+
+    __slots__ = ("dev", "ctx")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.dev = torch.cuda.device(device)
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return int(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return self.dev.__exit__(*exc)
+
+
+def _workspace(query, args, device):
+    """(tensor or None, pointer, bytes) of a call's working memory."""
+    n = ctypes.c_int64(0)
+    _check(query(*args, ctypes.byref(n)))
+    if n.value == 0:
+        return None, 0, 0
+    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), n.value
+
+
+def gated_scan_forward(x, log_a, reset=None, state_in=None, return_state=False, keep_chunks=False, y=None,
+                       stream=None):
+    """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t over x, log_a
+    [B, L, D] (float32 or bfloat16).  reset: [B, L] uint8 or None; state_in:
+    [B, D] float32 or None.  Returns y, followed by the final state [B, D] if
+    return_state and by the chunk states [B, ceil(L / 256), D] that
+    gated_scan_backward needs if keep_chunks.  y may be x."""
+    _main(x, "x")
+    B, L, D = x.shape
+    dev = x.device
+    _tensor(_required(log_a, "log_a"), "log_a", (B, L, D), x.dtype, dev)
+    _tensor(reset, "reset", (B, L), torch.uint8, dev)
+    _tensor(state_in, "state_in", (B, D), torch.float32, dev)
+    _check_outputs((y,), x)
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x)
+        state = torch.empty((B, D), dtype=torch.float32, device=dev) if return_state else None
+        chunks = torch.empty((B, -(-L // SCAN_CHUNK), D), dtype=torch.float32, device=dev) if keep_chunks else None
+        ws, wp, wn = _workspace(gecko_gated_scan_workspace, (B, L, D, _DT[x.dtype], 0), dev)
+        _check(gecko_gated_scan_forward(x.data_ptr(), log_a.data_ptr(), y.data_ptr(), _ptr(reset), _ptr(state_in),
+                                        _ptr(state), _ptr(chunks), B, L, D, _DT[x.dtype], wp, wn, st))
+    if not (return_state or keep_chunks):
+        return y
+    return (y,) + ((state,) if return_state else ()) + ((chunks,) if keep_chunks else ())
+
+
+def gated_scan_backward(x, log_a, dy, chunk_state, reset=None, dstate_out=None, stream=None):
+    """Gradients (dx, dlog_a, dstate_in) of gated_scan_forward for the output
+    gradient dy [B, L, D] and the final state's dstate_out [B, D] or None."""
+    _main(x, "x")
+    B, L, D = x.shape
+    dev = x.device
+    _tensor(_required(log_a, "log_a"), "log_a", (B, L, D), x.dtype, dev)
+    _tensor(_required(dy, "dy"), "dy", (B, L, D), x.dtype, dev)
+    _tensor(_required(chunk_state, "chunk_state"), "chunk_state", (B, -(-L // SCAN_CHUNK), D), torch.float32, dev)
+    _tensor(reset, "reset", (B, L), torch.uint8, dev)
+    _tensor(dstate_out, "dstate_out", (B, D), torch.float32, dev)
+    with _on(dev, stream) as st:
+        dx, dg = torch.empty_like(x), torch.empty_like(x)
+        ds = torch.empty((B, D), dtype=torch.float32, device=dev)
+        ws, wp, wn = _workspace(gecko_gated_scan_workspace, (B, L, D, _DT[x.dtype], 1), dev)
+        _check(gecko_gated_scan_backward(x.data_ptr(), log_a.data_ptr(), dy.data_ptr(), _ptr(reset),
+                                         chunk_state.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dg.data_ptr(),
+                                         ds.data_ptr(), B, L, D, _DT[x.dtype], wp, wn, st))
+    return dx, dg, ds
+
+
+def _qk_sizes(z, scale, pos):
+    _main(z, "z")
+    B, T, W = z.shape
+    if not (isinstance(scale, torch.Tensor) and scale.dim() == 3 and scale.shape[0] == 4
+            and scale.shape[1] * scale.shape[2] == W):
+        raise ValueError(f"scale must be [4, H, d] with H * d = {W}")
+    H, d = scale.shape[1:]
+    _tensor(scale, "scale", (4, H, d), torch.float32, z.device)
+    _tensor(pos, "pos", (B, T), torch.int64, z.device)
+    return B, T, H, d
+
+
+def qk_forward(z, scale, shift, eps: float = 1e-6, rot_dim: int = 0, rot_base: float = 10000.0,
+               interleaved: bool = False, pos=None, pos0: int = 0, stream=None):
+    """(q, k, qm, km) [B, H, T, d] from the shared representation z
+    [B, T, H d] (float32 or bfloat16): per-head norm, the four affines scale,
+    shift [4, H, d] float32, and q and k turned by position (rot_dim = 0: not).
+    pos: [B, T] int64, or None for pos0 + t."""
+    B, T, H, d = _qk_sizes(z, scale, pos)
+    dev = z.device
+    _tensor(_required(shift, "shift"), "shift", (4, H, d), torch.float32, dev)
+    with _on(dev, stream) as st:
+        outs = tuple(torch.empty((B, H, T, d), dtype=z.dtype, device=dev) for _ in range(4))
+        _check(gecko_qk_forward(z.data_ptr(), scale.data_ptr(), shift.data_ptr(), _ptr(pos),
+                                *(o.data_ptr() for o in outs), B, T, H, d, eps, pos0, rot_dim, rot_base,
+                                int(interleaved), _DT[z.dtype], st))
+    return outs
+
+
+def qk_backward(z, scale, dq, dk, dqm, dkm, eps: float = 1e-6, rot_dim: int = 0, rot_base: float = 10000.0,
+                interleaved: bool = False, pos=None, pos0: int = 0, stream=None):
+    """Gradients (dz [B, T, H d], dscale, dshift [4, H, d] float32) of
+    qk_forward for the gradients of its four outputs."""
+    B, T, H, d = _qk_sizes(z, scale, pos)
+    dev = z.device
+    grads = (dq, dk, dqm, dkm)
+    for g, name in zip(grads, ("dq", "dk", "dqm", "dkm")):
+        _tensor(_required(g, name), name, (B, H, T, d), z.dtype, dev)
+    with _on(dev, stream) as st:
+        dz, dscale, dshift = torch.empty_like(z), torch.empty_like(scale), torch.empty_like(scale)
+        ws, wp, wn = _workspace(gecko_qk_workspace, (B, T, H, d), dev)
+        _check(gecko_qk_backward(z.data_ptr(), scale.data_ptr(), _ptr(pos), *(g.data_ptr() for g in grads),
+                                 dz.data_ptr(), dscale.data_ptr(), dshift.data_ptr(), B, T, H, d, eps, pos0, rot_dim,
+                                 rot_base, int(interleaved), _DT[z.dtype], wp, wn, st))
+    return dz, dscale, dshift
+
+
+def _linear_sizes(x, w, act, heads):
+    """(B, T, N, K, shape of y); x is [B, T, K] or, without heads, [M, K]."""
+    flat = isinstance(x, torch.Tensor) and x.dim() == 2 and not heads
+    _main(x, "x", 2 if flat else 3)
+    K = x.shape[-1]
+    B, T = (1, x.shape[0]) if flat else x.shape[:2]
+    if not (isinstance(w, torch.Tensor) and w.dim() == 2 and w.shape[1] == K):
+        raise ValueError(f"w must be [N, {K}]")
+    N = w.shape[0]
+    _tensor(w, "w", (N, K), x.dtype, x.device)
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {tuple(ACTS)}")
+    if heads < 0 or (heads and N % heads):
+        raise ValueError(f"heads must divide N = {N}")
+    return B, T, N, K, (B, heads, T, N // heads) if heads else (*x.shape[:-1], N)
+
+
+def linear_forward(x, w, bias=None, residual=None, act: str = "none", heads: int = 0, keep_pre: bool = False,
+                   y=None, stream=None):
+    """y = f(x w^T + bias) + residual with f "none", "silu" or "gelu".  x:
+    [B, T, K] (or [M, K]); w: [N, K]; bias: [N] float32.  y and residual are
+    [B, T, N], or [B, heads, T, N / heads] if heads > 0.  Returns y, or
+    (y, pre) with x w^T + bias in y's layout if keep_pre."""
+    B, T, N, K, shape = _linear_sizes(x, w, act, heads)
+    dev = x.device
+    _tensor(bias, "bias", (N,), torch.float32, dev)
+    _tensor(residual, "residual", shape, x.dtype, dev)
+    _tensor(y, "y", shape, x.dtype, dev)
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=dev)
+        pre = torch.empty(shape, dtype=x.dtype, device=dev) if keep_pre else None
+        ws, wp, wn = _workspace(gecko_linear_workspace, (B, T, N, K, heads, ACTS[act], _DT[x.dtype], 0), dev)
+        _check(gecko_linear_forward(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre),
+                                    B, T, N, K, heads, ACTS[act], _DT[x.dtype], wp, wn, st))
+    return (y, pre) if keep_pre else y
+
+
+def linear_backward(x, w, dy, pre=None, act: str = "none", heads: int = 0, need=(True, True, True), stream=None):
+    """Gradients (dx, dw, db float32) of linear_forward for dy (y's layout);
+    pre as linear_forward kept it (needed for an activation).  need: which of
+    the three are wanted; the others are returned as None."""
+    B, T, N, K, shape = _linear_sizes(x, w, act, heads)
+    dev = x.device
+    _tensor(_required(dy, "dy"), "dy", shape, x.dtype, dev)
+    _tensor(pre, "pre", shape, x.dtype, dev)
+    with _on(dev, stream) as st:
+        dx = torch.empty_like(x) if need[0] else None
+        dw = torch.empty_like(w) if need[1] else None
+        db = torch.empty((N,), dtype=torch.float32, device=dev) if need[2] else None
+        ws, wp, wn = _workspace(gecko_linear_workspace, (B, T, N, K, heads, ACTS[act], _DT[x.dtype], 1), dev)
+        _check(gecko_linear_backward(x.data_ptr(), w.data_ptr(), dy.data_ptr(), _ptr(pre), _ptr(dx), _ptr(dw),
+                                     _ptr(db), B, T, N, K, heads, ACTS[act], _DT[x.dtype], wp, wn, st))
+    return dx, dw, db
+
+
+class GatedScanFunction(torch.autograd.Function):
+    """torch.autograd wrapper: (y, state) = GatedScanFunction.apply(x, log_a,
+    state_in or None, reset or None)."""
+
+    @staticmethod
+    def forward(ctx, x, log_a, state_in, reset):
+        y, state, chunks = gated_scan_forward(x, log_a, reset=reset, state_in=state_in, return_state=True,
+                                              keep_chunks=True)
+        ctx.save_for_backward(x, log_a, reset, chunks)
+        ctx.has_state = state_in is not None
+        return y, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dstate):
+        x, log_a, reset, chunks = ctx.saved_tensors
+        dx, dg, ds = gated_scan_backward(x, log_a, dy.contiguous(), chunks, reset=reset,
+                                         dstate_out=dstate.contiguous())
+        return dx, dg, ds if ctx.has_state else None, None
+
+
+class QkFunction(torch.autograd.Function):
+    """torch.autograd wrapper: (q, k, qm, km) = QkFunction.apply(z, scale,
+    shift, pos or None, options), options a dict of qk_forward's eps, rot_dim,
+    rot_base, interleaved, pos0."""
+
+    @staticmethod
+    def forward(ctx, z, scale, shift, pos, options):
+        ctx.save_for_backward(z, scale, pos)
+        ctx.options = dict(options)
+        return qk_forward(z, scale, shift, pos=pos, **options)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        z, scale, pos = ctx.saved_tensors
+        dz, dscale, dshift = qk_backward(z, scale, *(g.contiguous() for g in grads), pos=pos, **ctx.options)
+        return dz, dscale, dshift, None, None
+
+
+class LinearFunction(torch.autograd.Function):
+    """torch.autograd wrapper: y = LinearFunction.apply(x, w, bias or None,
+    residual or None, act, heads)."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act, heads):
+        keep = act != "none"
+        out = linear_forward(x, w, bias=bias, residual=residual, act=act, heads=heads, keep_pre=keep)
+        y, pre = out if keep else (out, None)
+        ctx.save_for_backward(x, w, pre)
+        ctx.act, ctx.heads = act, heads
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, pre = ctx.saved_tensors
+        dy = dy.contiguous()
+        need = ctx.needs_input_grad[:3]
+        grads = linear_backward(x, w, dy, pre=pre, act=ctx.act, heads=ctx.heads, need=need) if any(need) \
+            else (None, None, None)
+        return (*grads, dy if ctx.needs_input_grad[3] else None, None, None)
 
 
 # ------------------------------------------------ context parallelism -----
