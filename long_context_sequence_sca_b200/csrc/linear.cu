@@ -1,7 +1,12 @@
 // Projection y = f(x w^T + bias) + residual and its gradients:
 //   u = x w^T + bias,  du = dy (.) f'(u),
 //   dx = du w,  dw = du^T x,  db = column sums of du.
-// CUDA-core kernels for every type.
+// The kernels here are CUDA-core ones: the products for fp32 (and for bf16
+// under GECKO_KERNELS=simt), and the pass that forms du and db.  The bf16
+// products run on the tensor cores (linear_tc.cu).
+#include <cstdlib>
+#include <cstring>
+
 #include "common.cuh"
 #include "gecko_internal.h"
 #include "linear.cuh"
@@ -160,6 +165,16 @@ int64_t du_row_blocks(int64_t M, int64_t N) {
 // Whether dy itself is du, laid out as the products need it.
 bool dy_is_du(const LinearProblem& p) { return p.act == kActNone && p.H == 0; }
 
+size_t du_bytes(const LinearProblem& p) {
+  return dy_is_du(p) ? 0 : up256((p.dtype == kBF16 ? 2 : 4) * (size_t)p.M() * p.N);
+}
+
+// GECKO_KERNELS=simt selects the CUDA-core kernels for every type.
+bool use_tc(const LinearProblem& p) {
+  const char* e = std::getenv("GECKO_KERNELS");
+  return p.dtype == kBF16 && !(e && std::strcmp(e, "simt") == 0);
+}
+
 template <typename T>
 cudaError_t forward_simt(const LinearProblem& p, cudaStream_t st) {
   ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
@@ -174,7 +189,7 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   char* ws = static_cast<char*>(p.ws);
   const bool alias = dy_is_du(p);
   T* du = alias ? nullptr : reinterpret_cast<T*>(ws);
-  float* part = reinterpret_cast<float*>(ws + (alias ? 0 : up256(sizeof(T) * M * p.N)));
+  float* part = reinterpret_cast<float*>(ws + du_bytes(p));
   const bool products = p.dx || p.dw;
   if (p.db || (!alias && products)) {
     const int64_t blocks = du_row_blocks(M, p.N), rows = (M + blocks - 1) / blocks;
@@ -186,6 +201,13 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
       linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
   }
   const void* g = alias ? p.dy : du;
+  if (use_tc(p)) {
+    void* gws = ws + du_bytes(p) + up256(sizeof(float) * du_row_blocks(M, p.N) * p.N);
+    cudaError_t e;
+    if (p.dx && (e = launch_linear_dx_tc(p, g, gws, st))) return e;
+    if (p.dw && (e = launch_linear_dw_tc(p, g, gws, st))) return e;
+    return cudaGetLastError();
+  }
   if (p.dx)
     simt_gemm<T>(g, p.N, 1, p.w, 1, p.K, M, p.K, p.N, PlainOut<T>{static_cast<T*>(p.dx), p.K}, st);
   if (p.dw)
@@ -196,12 +218,16 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
 }  // namespace
 
 size_t linear_workspace_bytes(const LinearProblem& p, bool backward) {
-  if (!backward) return 0;
-  const size_t e = p.dtype == kBF16 ? 2 : 4;
-  return (dy_is_du(p) ? 0 : up256(e * p.M() * p.N)) + up256(sizeof(float) * du_row_blocks(p.M(), p.N) * p.N);
+  const bool tc = p.dtype == kBF16;
+  if (!backward) return tc ? gemm_tc_workspace(p.M(), p.N, p.K) : 0;
+  const size_t parts = up256(sizeof(float) * du_row_blocks(p.M(), p.N) * p.N);
+  if (!tc) return du_bytes(p) + parts;
+  const size_t dx = gemm_tc_workspace(p.M(), p.K, p.N), dw = gemm_tc_workspace(p.N, p.K, p.M());
+  return du_bytes(p) + parts + (dx > dw ? dx : dw);
 }
 
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st) {
+  if (use_tc(p)) return launch_linear_tc(p, st);
   return p.dtype == kBF16 ? forward_simt<__nv_bfloat16>(p, st) : forward_simt<float>(p, st);
 }
 

@@ -1,0 +1,565 @@
+// The projection's bf16 products on the 5th-generation tensor cores:
+//   C[m, n] = sum_k A(m, k) B(n, k)
+// with each operand stored along k (K-major) or along its own rows (MN-major),
+// which covers x w^T, du w and du^T x without a transposed copy.
+//
+// Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
+// ring of stages, one thread issues tcgen05.mma, four warps empty the
+// accumulator (TMEM, two of them in turn) through shared memory, where they
+// transpose it so that every global access is a run of 128 bytes of one row.
+// With CG = 2 a pair of CTAs shares one 256 x BN tile: each loads its 128
+// rows of A and half the rows of B, so a k-block moves half the bytes per
+// multiply-add of a 128 x BN tile; the even CTA issues the MMAs for both.
+#include "common.cuh"
+#include "gecko_internal.h"
+#include "linear.cuh"
+
+namespace gecko {
+namespace {
+
+// ---------------------------------------------------------- pair (CG = 2) --
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared-memory address of `p` in the CTA of rank `rank`.
+__device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait for a barrier on which another CTA of the cluster arrives.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else   // the barrier may lie in the other CTA of the pair
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 1)
+    umma_ss(d, a, b, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void umma_done(uint64_t* bar) {
+  if (CG == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_take(uint32_t* slot, uint32_t cols) {
+  if (CG == 1) {
+    tmem_alloc(slot, cols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_give(uint32_t taddr, uint32_t cols) {
+  if (CG == 1)
+    tmem_dealloc(taddr, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+
+// ------------------------------------------------------------- work split --
+
+constexpr int kBK = 64;              // k-block: one 128-byte swizzle row
+constexpr int kGemmThreads = 256;    // TMA, MMA, TMEM, idle warp; four epilogue warps
+constexpr int kEpilogueWarp = 4;
+constexpr int kGroupM = 8;           // tiles of one column band done together (operand reuse in L2)
+
+struct GemmShape {
+  int64_t M, N;
+  int tiles_m, tiles_n, k_blocks;
+  int splits, blocks_per_split;   // the k-blocks in `splits` runs, each its own unit
+};
+
+struct Unit {
+  int m, n, split, kb0, kb1;
+};
+
+__device__ __forceinline__ Unit unit_at(const GemmShape& g, int u) {
+  const int tiles = g.tiles_m * g.tiles_n;
+  Unit r;
+  r.split = u / tiles;
+  const int t = u - r.split * tiles;
+  const int band = kGroupM * g.tiles_n, group = t / band, in = t - group * band;
+  const int m0 = group * kGroupM, gm = min(kGroupM, g.tiles_m - m0);
+  r.n = in / gm;
+  r.m = m0 + (in - r.n * gm);
+  r.kb0 = r.split * g.blocks_per_split;
+  r.kb1 = min(g.k_blocks, r.kb0 + g.blocks_per_split);
+  return r;
+}
+
+// -------------------------------------------------------------- epilogues --
+
+// Each gives, for 8 consecutive columns n of row m, what is written.  Row and
+// column parts of an address are separate: rows are fixed for a tile.
+
+struct EpiForward {
+  const float* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16 *y, *pre;
+  int N, T, H, hd, act;
+  __device__ __forceinline__ int64_t row(int64_t m) const {
+    if (H == 0) return m * N;
+    const uint32_t b = (uint32_t)m / (uint32_t)T, t = (uint32_t)m - b * (uint32_t)T;
+    return ((int64_t)b * H * T + t) * hd;
+  }
+  __device__ __forceinline__ int64_t col(int n) const {
+    if (H == 0) return n;
+    const int h = n / hd;
+    return (int64_t)h * T * hd + (n - h * hd);
+  }
+  __device__ __forceinline__ void put(int64_t row, int64_t col, int n, int /*split*/, float (&v)[8]) const {
+    if (bias) {
+      float b[8];
+      load_f8(bias + n, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    const int64_t at = row + col;
+    if (pre) store_f8(pre + at, v);
+    if (act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], act);
+    }
+    if (residual) {
+      float r[8];
+      load_f8(residual + at, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+    store_f8(y + at, v);
+  }
+};
+
+struct EpiPlain {
+  __nv_bfloat16* c;
+  int N;
+  __device__ __forceinline__ int64_t row(int64_t m) const { return m * N; }
+  __device__ __forceinline__ int64_t col(int n) const { return n; }
+  __device__ __forceinline__ void put(int64_t row, int64_t col, int, int, float (&v)[8]) const {
+    store_f8(c + row + col, v);
+  }
+};
+
+struct EpiPartial {
+  float* part;   // [splits, M, N]
+  int64_t M;
+  int N;
+  __device__ __forceinline__ int64_t row(int64_t m) const { return m * N; }
+  __device__ __forceinline__ int64_t col(int n) const { return n; }
+  __device__ __forceinline__ void put(int64_t row, int64_t col, int, int split, float (&v)[8]) const {
+    store_f8(part + (int64_t)split * M * N + row + col, v);
+  }
+};
+
+// ----------------------------------------------------------------- kernel --
+
+template <int CG, int BN>
+struct GemmCfg {
+  static constexpr int kA = 128 * kBK * 2, kB = BN / CG * kBK * 2, kStage = kA + kB;
+  static constexpr int kStaging = 4 * 32 * 64 * 4;   // per epilogue warp: 32 rows x 64 columns, fp32
+  static constexpr int kStages = (232448 - 1024 - 512 - kStaging) / kStage > 8
+                                     ? 8 : (232448 - 1024 - 512 - kStaging) / kStage;
+  static constexpr int kStageOff = kStages * kStage;
+  static constexpr int kBarOff = kStageOff + kStaging;
+  static constexpr int kNumBars = 2 * kStages + 4;   // full, empty; accumulator full, empty
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kAlloc = kMiscOff + 16 + 1024;
+  static constexpr uint32_t kTmemCols = 2 * BN;
+  static_assert(kAlloc <= 232448, "shared memory above the per-block limit");
+};
+
+template <int CG, int BN, bool AMN, bool BMN, class Epi>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_constant__ CUtensorMap ma,
+                                                                  const __grid_constant__ CUtensorMap mb,
+                                                                  const GemmShape g, const Epi ep, int* status) {
+  using Cfg = GemmCfg<CG, BN>;
+  constexpr int NS = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);   // used in the even CTA
+  uint64_t* empty = full + NS;
+  uint64_t* acc_full = empty + NS;    // [2]
+  uint64_t* acc_empty = acc_full + 2; // [2], used in the even CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kMiscOff + 4);
+
+  const int warp = warp_id_uniform(), lane = threadIdx.x % 32;
+  const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  const int units = g.tiles_m * g.tiles_n * g.splits;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 4 * CG);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_take<CG>(tmem_slot, Cfg::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- TMA producer --
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step) {
+        const Unit t = unit_at(g, u);
+        const int m0 = (t.m * CG + (int)rank) * 128, n0 = t.n * BN + (int)rank * (BN / CG);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = it % NS;
+          if (it >= NS && !(ok = mbar_wait_cluster(empty + s, (it / NS - 1) & 1, abort_flag, status))) break;
+          if (rank == 0) mbar_arrive_expect_tx(full + s, CG * Cfg::kStage);
+          const uint32_t bar = CG == 1 ? smem_u32(full + s) : map_to(full + s, 0);
+          uint8_t *pa = smem + s * Cfg::kStage, *pb = pa + Cfg::kA;
+          if (AMN) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tma_load<CG>(pa + i * 8192, &ma, bar, m0 + 64 * i, kb * kBK);
+          } else {
+            tma_load<CG>(pa, &ma, bar, kb * kBK, m0);
+          }
+          if (BMN) {
+#pragma unroll
+            for (int i = 0; i < BN / CG / 64; ++i) tma_load<CG>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK);
+          } else {
+            tma_load<CG>(pb, &mb, bar, kb * kBK, n0);
+          }
+        }
+      }
+      // the stages' last readers, so that nothing arrives here after the exit;
+      // after an abort, the copies issued (both CTAs' land on the even one's barriers)
+      for (int i = it > NS ? it - NS : 0; i < it; ++i) {
+        if (*abort_flag) {
+          if (rank == 0) mbar_wait_drain(full + i % NS, (i / NS) & 1);
+        } else {
+          mbar_wait_cluster(empty + i % NS, (i / NS) & 1, abort_flag, status);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128 * CG, BN, AMN, BMN);
+      const uint32_t base = smem_u32(smem);
+      int it = 0, k = 0;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step, ++k) {
+        const Unit t = unit_at(g, u);
+        const int acc = k & 1;
+        if (k >= 2 && !(ok = mbar_wait_cluster(acc_empty + acc, (k / 2 - 1) & 1, abort_flag, status))) break;
+        tc_fence_after();
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = it % NS;
+          if (!(ok = mbar_wait_cluster(full + s, (it / NS) & 1, abort_flag, status))) break;
+          tc_fence_after();
+          const uint32_t a0 = base + s * Cfg::kStage, b0 = a0 + Cfg::kA;
+          const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
+          const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            umma<CG>(tmem + acc * BN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
+                     idesc, kb > t.kb0 || kk > 0 ? 1u : 0u);
+          umma_done<CG>(empty + s);
+        }
+        if (ok) umma_done<CG>(acc_full + acc);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kEpilogueWarp) {
+    // ----------------------------------------------------------- epilogue --
+    const int q = warp - kEpilogueWarp;   // TMEM lane quarter (warp % 4)
+    float* stage = reinterpret_cast<float*>(smem + Cfg::kStageOff) + q * 32 * 64;
+    const int c8 = lane % 8, r4 = lane / 8;
+    int k = 0;
+    bool ok = true;
+    for (int u = first; u < units; u += step, ++k) {
+      const Unit t = unit_at(g, u);
+      const int acc = k & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full + acc, (k / 2) & 1, abort_flag, status));
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t m0 = ((int64_t)t.m * CG + rank) * 128 + q * 32;
+      const int n0 = t.n * BN;
+      int64_t row[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) row[i] = ep.row(m0 + 4 * i + r4);
+      const uint32_t from = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < BN / 64; ++c) {
+        uint32_t v[64];
+        tmem_ld32p(from + c * 64, v);
+        tmem_ld32p(from + c * 64 + 32, v + 32);
+        tmem_wait_ld();
+        if (c == BN / 64 - 1) {
+          // the accumulator is read: the MMAs of the unit after next may write it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(CG == 1 ? smem_u32(acc_empty + acc) : map_to(acc_empty + acc, 0));
+        }
+        // lane = row; 16-byte piece j of a row lies at (even pieces, then odd) ^ row: no bank conflicts
+        // here, nor below where 8 lanes read one row
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((((j >> 1) | ((j & 1) << 3)) ^ (lane & 7)) << 2)) =
+              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+        const int n = n0 + c * 64 + c8 * 8;
+        if (n < g.N) {
+          const int64_t col = ep.col(n);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + r4;
+            if (m0 + r < g.M) {
+              const float* p = stage + r * 64;
+              const float4 lo = *reinterpret_cast<const float4*>(p + ((c8 ^ (r & 7)) << 2));
+              const float4 hi = *reinterpret_cast<const float4*>(p + (((c8 + 8) ^ (r & 7)) << 2));
+              float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              ep.put(row[i], col, n, t.split, w);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  if (warp == 2) tmem_give<CG>(tmem, Cfg::kTmemCols);
+  if (CG == 2) cluster_sync();
+}
+
+// Sum of the splits' partial products, then the epilogue.
+template <class Epi>
+__global__ void __launch_bounds__(256) gemm_sum_kernel(const float* part, int splits, int64_t M, int N, const Epi ep) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= M * N) return;
+  const int64_t m = i / N;
+  const int n = (int)(i - m * N);
+  float v[8];
+  load_f8(part + i, v);
+  for (int s = 1; s < splits; ++s) {
+    float w[8];
+    load_f8(part + (int64_t)s * M * N + i, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += w[j];
+  }
+  ep.put(ep.row(m), ep.col(n), n, 0, v);
+}
+
+// ------------------------------------------------------------------- host --
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(p)
+               : nullptr;
+  }();
+  return fn;
+}
+
+// [rows, inner] bf16 row-major, boxes of 64 x box_rows with 128-byte swizzle;
+// what lies outside reads as zero.
+cudaError_t make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t inner, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct Operand {
+  const void* p;
+  bool mn;   // stored [k, rows] instead of [rows, k]
+};
+
+struct GemmPlan {
+  int cg, bn;
+  GemmShape g;
+};
+
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K) {
+  GemmPlan pl;
+  pl.cg = 2;
+  pl.bn = 256;
+  auto tiles = [&](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
+  if ((int64_t)tiles(M, 256) * tiles(N, 256) < sm_count() / 2) {
+    pl.cg = 1;
+    pl.bn = 128;
+  }
+  pl.g.M = M;
+  pl.g.N = N;
+  pl.g.tiles_m = tiles(M, 128 * pl.cg);
+  pl.g.tiles_n = tiles(N, pl.bn);
+  pl.g.k_blocks = tiles(K, kBK);
+  const int slots = sm_count() / pl.cg, t = pl.g.tiles_m * pl.g.tiles_n;
+  int splits = slots / t;
+  if (splits > pl.g.k_blocks / 8) splits = pl.g.k_blocks / 8;
+  if (splits < 1) splits = 1;
+  pl.g.blocks_per_split = (pl.g.k_blocks + splits - 1) / splits;
+  pl.g.splits = (pl.g.k_blocks + pl.g.blocks_per_split - 1) / pl.g.blocks_per_split;
+  return pl;
+}
+
+template <int CG, int BN, bool AMN, bool BMN, class Epi>
+cudaError_t run_gemm(const GemmPlan& pl, const Operand& A, const Operand& B, int64_t K, const Epi& ep, int* status,
+                     cudaStream_t st) {
+  using Cfg = GemmCfg<CG, BN>;
+  CUtensorMap ma, mb;
+  cudaError_t e;
+  const GemmShape& g = pl.g;
+  if ((e = AMN ? make_map(&ma, A.p, K, g.M, kBK) : make_map(&ma, A.p, g.M, K, 128))) return e;
+  if ((e = BMN ? make_map(&mb, B.p, K, g.N, kBK) : make_map(&mb, B.p, g.N, K, BN / CG))) return e;
+  auto kern = gemm_tc_kernel<CG, BN, AMN, BMN, Epi>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kAlloc))) return e;
+  const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  const int64_t slots = sm_count() / CG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CG * (units < slots ? units : slots)));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = Cfg::kAlloc;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g, ep, status);
+}
+
+template <bool AMN, bool BMN, class Epi>
+cudaError_t gemm_of(const GemmPlan& pl, const Operand& A, const Operand& B, int64_t K, const Epi& ep, int* status,
+                    cudaStream_t st) {
+  return pl.cg == 2 ? run_gemm<2, 256, AMN, BMN, Epi>(pl, A, B, K, ep, status, st)
+                    : run_gemm<1, 128, AMN, BMN, Epi>(pl, A, B, K, ep, status, st);
+}
+
+template <bool AMN, bool BMN, class Epi>
+cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const Epi& ep, void* ws, int* status,
+                 cudaStream_t st) {
+  const GemmPlan pl = gemm_plan(M, N, K);
+  const Operand a{A, AMN}, b{B, BMN};
+  if (pl.g.splits == 1) return gemm_of<AMN, BMN>(pl, a, b, K, ep, status, st);
+  float* part = static_cast<float*>(ws);
+  if (cudaError_t e = gemm_of<AMN, BMN>(pl, a, b, K, EpiPartial{part, M, (int)N}, status, st)) return e;
+  gemm_sum_kernel<Epi><<<(unsigned)((M * N / 8 + 255) / 256), 256, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K) {
+  const GemmPlan pl = gemm_plan(M, N, K);
+  return pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
+}
+
+cudaError_t launch_linear_tc(const LinearProblem& p, cudaStream_t st) {
+  const EpiForward ep{p.bias,   static_cast<const __nv_bfloat16*>(p.residual),
+                      static_cast<__nv_bfloat16*>(p.y), static_cast<__nv_bfloat16*>(p.pre),
+                      (int)p.N, (int)p.T, (int)p.H, p.H ? (int)(p.N / p.H) : 1, p.act};
+  return gemm<false, false>(p.M(), p.N, p.K, p.x, p.w, ep, p.ws, p.status, st);
+}
+
+cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, void* ws, cudaStream_t st) {
+  return gemm<false, true>(p.M(), p.K, p.N, du, p.w, EpiPlain{static_cast<__nv_bfloat16*>(p.dx), (int)p.K}, ws,
+                           p.status, st);
+}
+
+cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, void* ws, cudaStream_t st) {
+  return gemm<true, true>(p.N, p.K, p.M(), du, p.x, EpiPlain{static_cast<__nv_bfloat16*>(p.dw), (int)p.K}, ws,
+                          p.status, st);
+}
+
+}  // namespace gecko

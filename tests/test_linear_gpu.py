@@ -78,6 +78,12 @@ def test_matches_oracle(L, B, T, N, K, H, dtype):
     check(L, _inputs(B, T, N, K, H, dtype, seed=T * 31 + N * 7 + K), dtype, act, H)
 
 
+@pytest.mark.parametrize("B,T,N,K,H,act", [(5, 500, 2048, 2056, 16, "silu"), (1, 2700, 2184, 2048, 0, "none")])
+def test_many_tiles(L, B, T, N, K, H, act):
+    """Enough output tiles, in every product, for the large tiles shared by two CTAs; several per CTA."""
+    check(L, _inputs(B, T, N, K, H, "bf16", seed=3), "bf16", act, H)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("bias,residual,H", [(True, False, 0), (False, True, 4), (False, False, 0), (True, True, 2)])
