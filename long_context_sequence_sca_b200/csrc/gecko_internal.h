@@ -229,6 +229,7 @@ struct ScanProblem {
   int* status;
 };
 
+bool scan_grid_fits(int64_t B, int64_t L, int64_t D, int dtype);   // one block per tile
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype, bool backward);
 cudaError_t launch_scan(const ScanProblem& p, cudaStream_t st);
 cudaError_t launch_scan_bwd(const ScanProblem& p, cudaStream_t st);

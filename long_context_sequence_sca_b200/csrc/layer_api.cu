@@ -67,7 +67,7 @@ int check_scan_sizes(int64_t B, int64_t L, int64_t D, int dtype) {
   if (B < 1 || L < 1 || D < 1)
     return fail(GECKO_ERR_ARG, "sizes must be >= 1 (B=%lld L=%lld D=%lld)", (long long)B, (long long)L, (long long)D);
   if (D % 8) return fail(GECKO_ERR_SHAPE, "D must be a multiple of 8 (got %lld)", (long long)D);
-  if (B > kGridYZ || L > kGridYZ * kScanChunk || D > (int64_t(1) << 24) || (long double)B * L * D > 1.0e18L)
+  if (B > kGridYZ || L > kGridYZ * kScanChunk || D > (int64_t(1) << 24) || !scan_grid_fits(B, L, D, dtype))
     return fail(GECKO_ERR_SHAPE, "B, L or D exceeds the kernels' range (B=%lld L=%lld D=%lld)", (long long)B,
                 (long long)L, (long long)D);
   return GECKO_OK;

@@ -7,161 +7,561 @@
 // A span of tokens maps the state entering it affinely, h_out = A h_in + h,
 // with A the product of its decays and h its scan from zero; spans compose.
 // Everything is held in fp32 whatever the tensors' type.
+//
+// The work is bound by HBM (3 values per element forward, 5 backward), so a
+// tile of one chunk (256 tokens) by 128 bytes of features is read once, by TMA,
+// into shared memory and scanned there: warp w takes tokens 32 w .. 32 w + 31,
+// a lane the features of 4 bytes.  First every warp finds the map of its span,
+// then the state entering the chunk is fetched, then every warp scans again
+// from its own entering state.  Chunks hand the state on in one launch: blocks
+// draw tiles in chunk order from a counter, so every tile that a block waits
+// for is held by a block that already runs.  A chunk publishes its map as soon
+// as it has it; the state entering chunk c is folded, in chunk order, from the
+// state entering its group of 16 chunks and the maps of the chunks between, so
+// the chain of dependent hand-offs is 16 times shorter than the chain of
+// chunks, and the association, and with it every bit of the result, does not
+// depend on timing.
 #include "common.cuh"
 #include "gecko_internal.h"
 
 namespace gecko {
 namespace {
 
+constexpr int kWarps = 8, kSpan = kScanChunk / kWarps;   // tokens per warp: 32, one reset bit each in a word
+constexpr int kThreads = 32 * kWarps;
+constexpr int kGroup = 16;                               // chunks per group of the hand-off
+constexpr int kRowBytes = 128;                           // features per tile, in bytes
+constexpr int kTileBytes = kScanChunk * kRowBytes;
+static_assert(kSpan == 32, "a span's document starts are one 32-bit word");
+
+// Features per lane and per tile.
+template <typename T> constexpr int kV = 4 / (int)sizeof(T);
+template <typename T> constexpr int kFT = 32 * kV<T>;
+
+__device__ __forceinline__ void read4(const uint8_t* p, float (&v)[2]) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+  v[0] = __uint_as_float(u << 16);
+  v[1] = __uint_as_float(u & 0xffff0000u);
+}
+__device__ __forceinline__ void read4(const uint8_t* p, float (&v)[1]) { v[0] = *reinterpret_cast<const float*>(p); }
+__device__ __forceinline__ void write4(uint8_t* p, const float (&v)[2]) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+}
+__device__ __forceinline__ void write4(uint8_t* p, const float (&v)[1]) { *reinterpret_cast<float*>(p) = v[0]; }
+
 // A decay of zero drops what came before, even if that is not finite.
 __device__ __forceinline__ float decay_fma(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
 
-__device__ __forceinline__ float decay_of(float log_a, bool drop) { return drop ? 0.f : expf(log_a); }
+// exp(log_a): for bf16 gates the SFU's 2^x (2^-22 relative, and |log_a| 2^-24
+// from the scaled argument); fp32 gates take the full expf, whose error stays
+// at 2^-23 however many tokens multiply it.
+__device__ __forceinline__ float gate(float log_a, __nv_bfloat16) { return ex2(log_a * kLog2e); }
+__device__ __forceinline__ float gate(float log_a, float) { return expf(log_a); }
 
-// (A, h) of every chunk scanned from zero: agg [B, C, D].
+struct ScanArgs {
+  const uint8_t* reset;
+  const float* enter0;    // state entering the first chunk of the walk (rows enter0_stride apart), or null
+  int64_t enter0_stride;
+  float* leave;           // [B, D] state leaving the last, or null
+  float* chunk_state;     // [B, C, D]
+  int64_t L, D;
+  int B, C, tiles;        // tiles of features
+  // hand-off (ws): [0] the counter, [1] the abort flag, then one flag per
+  // (b, tile, chunk of the walk); maps (A, h) [B, C, D]; group states [B, G, D]
+  int* sync;
+  float2* map;
+  float* group;
+  int* status;
+};
+
+struct Tile {
+  int c, b, tile;   // chunk along the walk
+};
+
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(int* p, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ int* flag_of(const ScanArgs& a, const Tile& t, int c) {
+  return a.sync + 2 + ((int64_t)t.b * a.tiles + t.tile) * a.C + c;
+}
+
+// One warp: publish the chunk's map, wait for what precedes it, and return the
+// state entering the chunk in h; publish the state entering the next group.
+// False if a wait ran out.
+template <int V>
+__device__ __forceinline__ bool hand_off(const ScanArgs& a, const Tile& t, int64_t d, bool on, const float (&A)[V],
+                                         const float (&m)[V], float (&h)[V]) {
+  const int lane = threadIdx.x & 31;
+  const int first = t.c / kGroup * kGroup, n = t.c - first;   // chunks of the group before this one
+  const bool last_of_group = n == kGroup - 1 && t.c + 1 < a.C;
+  const int64_t row = (int64_t)t.b * a.C;
+  if (n < kGroup - 1 && t.c + 1 < a.C) {
+    if (on)
+#pragma unroll
+      for (int i = 0; i < V; ++i) __stcg(a.map + (row + t.c) * a.D + d + i, make_float2(A[i], m[i]));
+    __syncwarp();
+    if (lane == 0) {
+      __threadfence();
+      store_release(flag_of(a, t, t.c), 1);
+    }
+  }
+  // lane l < n: the map of chunk first + l; lane 31: the state entering the group
+  const int* want = lane < n ? flag_of(a, t, first + lane) : lane == 31 && first ? flag_of(a, t, first - 1) : nullptr;
+  bool ready = !want || load_acquire(want) != 0;
+  if (!__all_sync(0xffffffffu, ready)) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (!ready) ready = load_acquire(want) != 0;
+      if (__all_sync(0xffffffffu, ready)) break;
+      if ((it & 63u) == 0) {
+        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late || load_acquire(a.sync + 1))) {
+          if (lane == 0) {
+            store_release(a.sync + 1, 1);
+            atomicOr(a.status, kStatusTimeout);
+          }
+          return false;
+        }
+      }
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = 0.f;
+  if (on) {
+    const int64_t bd = (int64_t)t.b * a.D + d;
+    if (first) {
+      const int64_t G = (a.C + kGroup - 1) / kGroup;
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = __ldcg(a.group + ((int64_t)t.b * G + first / kGroup) * a.D + d + i);
+    } else if (a.enter0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = a.enter0[t.b * a.enter0_stride + d + i];
+    }
+    // loads five ahead of their folds (all fifteen would spill)
+#pragma unroll
+    for (int c0 = 0; c0 < kGroup - 1; c0 += 5) {
+      float2 am[5][V];
+#pragma unroll
+      for (int c = 0; c < 5; ++c)
+        if (c0 + c < n)
+#pragma unroll
+          for (int i = 0; i < V; ++i) am[c][i] = __ldcg(a.map + (row + first + c0 + c) * a.D + d + i);
+#pragma unroll
+      for (int c = 0; c < 5; ++c)
+        if (c0 + c < n)
+#pragma unroll
+          for (int i = 0; i < V; ++i) h[i] = decay_fma(am[c][i].x, h[i], am[c][i].y);
+    }
+    if (last_of_group) {
+      const int64_t G = (a.C + kGroup - 1) / kGroup;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        __stcg(a.group + ((int64_t)t.b * G + first / kGroup + 1) * a.D + d + i, decay_fma(A[i], h[i], m[i]));
+    }
+    if (t.c + 1 == a.C && a.leave) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) a.leave[bd + i] = decay_fma(A[i], h[i], m[i]);
+    }
+  }
+  __syncwarp();
+  if (last_of_group && lane == 0) {
+    __threadfence();
+    store_release(flag_of(a, t, t.c), 1);
+  }
+  return true;
+}
+
 template <typename T>
-__global__ void scan_local_kernel(const T* x, const T* log_a, const uint8_t* reset, float2* agg, int64_t L, int64_t D) {
-  const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= D) return;
-  const int64_t b = blockIdx.z, c = blockIdx.y;
-  const int64_t t0 = c * kScanChunk, t1 = min(L, t0 + kScanChunk);
-  float A = 1.f, h = 0.f;
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t i = (b * L + t) * D + d;
-    const float a = decay_of(to_f32(log_a[i]), reset && reset[b * L + t]);
-    h = decay_fma(a, h, to_f32(x[i]));
-    A *= a;
-  }
-  agg[(b * gridDim.y + c) * D + d] = make_float2(A, h);
+struct ScanSmem {
+  float2 map[kWarps][kFT<T>];    // (A, h) of every warp's span
+  float2 back[kWarps][kFT<T>];   // backward: the same of the reverse recurrence
+  float enter[kFT<T>], enter_back[kFT<T>];
+  uint64_t bar;
+  int abort_flag, unit, ok;
+};
+
+// Which tile this block takes: drawn from the counter, or (one chunk: nothing
+// to wait for) the block's own index.
+__device__ __forceinline__ Tile draw_tile(const ScanArgs& a, int* slot) {
+  if (threadIdx.x == 0) *slot = a.C > 1 ? atomicAdd(a.sync, 1) : (int)blockIdx.x;
+  __syncthreads();
+  const int u = *slot, per_chunk = a.B * a.tiles;
+  Tile t;
+  t.c = u / per_chunk;
+  const int r = u - t.c * per_chunk;
+  t.b = r / a.tiles;
+  t.tile = r - t.b * a.tiles;
+  return t;
 }
 
-// State entering every chunk, and the state after the last one.
-__global__ void scan_carry_kernel(const float2* agg, const float* state_in, float* enter, float* state_out, int64_t B,
-                                  int64_t C, int64_t D) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= B * D) return;
-  const int64_t b = i / D, d = i % D;
-  float h = state_in ? state_in[i] : 0.f;
-  for (int64_t c = 0; c < C; ++c) {
-    const int64_t j = (b * C + c) * D + d;
-    enter[j] = h;
-    h = decay_fma(agg[j].x, h, agg[j].y);
-  }
-  if (state_out) state_out[i] = h;
+// Bit s: a document starts at token t0 + s.
+__device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int b, int64_t t0) {
+  const int lane = threadIdx.x & 31;
+  const bool start = a.reset && t0 + lane < a.L && a.reset[(int64_t)b * a.L + t0 + lane];
+  return __ballot_sync(0xffffffffu, start);
+}
+
+// The gates of token s of a span.
+template <typename T>
+__device__ __forceinline__ void gates(const uint8_t* row, uint32_t starts, int s, float (&a)[kV<T>]) {
+  read4(row, a);
+#pragma unroll
+  for (int i = 0; i < kV<T>; ++i) a[i] = starts >> s & 1u ? 0.f : gate(a[i], T());
+}
+
+// Map of the chunk and, for this thread's span, of what precedes it in the chunk.
+template <int V, int F>
+__device__ __forceinline__ void fold(const float2 (&map)[kWarps][F], int f, int from, int to, int step, float (&A)[V],
+                                     float (&h)[V]) {
+  for (int w = from; w != to; w += step)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 m = map[w][f + i];
+      h[i] = decay_fma(m.x, h[i], m.y);
+      A[i] *= m.x;
+    }
 }
 
 template <typename T>
-__global__ void scan_out_kernel(const T* x, const T* log_a, const uint8_t* reset, const float* enter, T* y, int64_t L,
-                                int64_t D) {
-  const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= D) return;
-  const int64_t b = blockIdx.z, c = blockIdx.y;
-  const int64_t t0 = c * kScanChunk, t1 = min(L, t0 + kScanChunk);
-  float h = enter[(b * gridDim.y + c) * D + d];
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t i = (b * L + t) * D + d;
-    const float a = decay_of(to_f32(log_a[i]), reset && reset[b * L + t]);
-    h = decay_fma(a, h, to_f32(x[i]));
-    y[i] = from_f32<T>(h);
+__global__ void __launch_bounds__(kThreads, 3) scan_kernel(const __grid_constant__ CUtensorMap mx,
+                                                           const __grid_constant__ CUtensorMap mg,
+                                                           const __grid_constant__ CUtensorMap my, const ScanArgs a) {
+  constexpr int V = kV<T>, F = kFT<T>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tx = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* tg = tx + kTileBytes;
+  __shared__ ScanSmem<T> sm;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    mbar_init(&sm.bar, 1);
+    fence_mbar_init();
+  }
+  const Tile t = draw_tile(a, &sm.unit);
+  const int64_t t0 = (int64_t)t.c * kScanChunk;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(&sm.bar, 2 * kTileBytes);
+    tma_load_3d(tx, &mx, &sm.bar, t.tile * F, (int)t0, t.b);
+    tma_load_3d(tg, &mg, &sm.bar, t.tile * F, (int)t0, t.b);
+  }
+  const uint32_t starts = start_bits(a, t.b, t0 + warp * kSpan);
+  const bool loaded = mbar_wait(&sm.bar, 0, &sm.abort_flag, a.status);
+  if (__syncthreads_or(!loaded)) {
+    mbar_wait_drain(&sm.bar, 0);
+    return;
+  }
+  uint8_t *px = tx + warp * kSpan * kRowBytes + lane * 4, *pg = tg + warp * kSpan * kRowBytes + lane * 4;
+  const int f = lane * V;
+  {
+    // tokens past the end read as zeros: a = 1, x = 0, the identity
+    float A[V], h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 1.f, h[i] = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < kSpan; ++s) {
+      float g[V], x[V];
+      gates<T>(pg + s * kRowBytes, starts, s, g);
+      read4(px + s * kRowBytes, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[i] = decay_fma(g[i], h[i], x[i]);
+        A[i] *= g[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sm.map[warp][f + i] = make_float2(A[i], h[i]);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float A[V], m[V], h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 1.f, m[i] = 0.f;
+    fold<V, F>(sm.map, f, 0, kWarps, 1, A, m);
+    const int64_t d = (int64_t)t.tile * F + f;
+    const bool ok = hand_off<V>(a, t, d, d < a.D, A, m, h);
+    if (ok && a.chunk_state && d < a.D) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) a.chunk_state[((int64_t)t.b * a.C + t.c) * a.D + d + i] = h[i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sm.enter[f + i] = h[i];
+    if (lane == 0) sm.ok = ok;
+  }
+  __syncthreads();
+  if (!sm.ok) return;
+  float A[V], h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = sm.enter[f + i], A[i] = 1.f;
+  fold<V, F>(sm.map, f, 0, warp, 1, A, h);
+#pragma unroll 8
+  for (int s = 0; s < kSpan; ++s) {
+    float g[V], x[V];
+    gates<T>(pg + s * kRowBytes, starts, s, g);
+    read4(px + s * kRowBytes, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = decay_fma(g[i], h[i], x[i]);
+    write4(px + s * kRowBytes, h);   // y over the consumed x
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    tma_store_3d(&my, tx, t.tile * F, (int)t0, t.b);
+    bulk_commit();
+    bulk_wait_read_all();
   }
 }
 
-// Reverse direction: with e_t = a_t dh_t (what token t passes back),
-// e = A e_next + r over a chunk: dh_t = dy_t + e_{t+1}.
+// The backward walks the chunks from the last to the first.  A warp finds the
+// maps of both recurrences over its span in one ascending pass: with P_t the
+// product of the span's gates up to t, what the span passes back is
+// e = sum_t P_t dy_t + P e_next.  Then it scans forward again, keeping the 32
+// states h_{t-1} in registers, and back over them.
 template <typename T>
-__global__ void scan_bwd_local_kernel(const T* dy, const T* log_a, const uint8_t* reset, float2* agg, int64_t L,
-                                      int64_t D) {
-  const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= D) return;
-  const int64_t b = blockIdx.z, c = blockIdx.y;
-  const int64_t t0 = c * kScanChunk, t1 = min(L, t0 + kScanChunk);
-  float A = 1.f, e = 0.f;
-  for (int64_t t = t1 - 1; t >= t0; --t) {
-    const int64_t i = (b * L + t) * D + d;
-    const float a = decay_of(to_f32(log_a[i]), reset && reset[b * L + t]);
-    e = a == 0.f ? 0.f : a * (to_f32(dy[i]) + e);
-    A *= a;
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const __grid_constant__ CUtensorMap mx,
+                                                               const __grid_constant__ CUtensorMap mg,
+                                                               const __grid_constant__ CUtensorMap mdy,
+                                                               const __grid_constant__ CUtensorMap mdx,
+                                                               const __grid_constant__ CUtensorMap mdg,
+                                                               const ScanArgs a) {
+  constexpr int V = kV<T>, F = kFT<T>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tx = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t *tg = tx + kTileBytes, *td = tg + kTileBytes;
+  __shared__ ScanSmem<T> sm;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    mbar_init(&sm.bar, 1);
+    fence_mbar_init();
   }
-  agg[(b * gridDim.y + c) * D + d] = make_float2(A, e);
+  const Tile t = draw_tile(a, &sm.unit);
+  const int c = a.C - 1 - t.c;
+  const int64_t t0 = (int64_t)c * kScanChunk;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(&sm.bar, 3 * kTileBytes);
+    tma_load_3d(tx, &mx, &sm.bar, t.tile * F, (int)t0, t.b);
+    tma_load_3d(tg, &mg, &sm.bar, t.tile * F, (int)t0, t.b);
+    tma_load_3d(td, &mdy, &sm.bar, t.tile * F, (int)t0, t.b);
+  }
+  const int f = lane * V;
+  const int64_t d = (int64_t)t.tile * F + f;
+  const uint32_t starts = start_bits(a, t.b, t0 + warp * kSpan);
+  float h0[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) h0[i] = d < a.D ? a.chunk_state[((int64_t)t.b * a.C + c) * a.D + d + i] : 0.f;
+  const bool loaded = mbar_wait(&sm.bar, 0, &sm.abort_flag, a.status);
+  if (__syncthreads_or(!loaded)) {
+    mbar_wait_drain(&sm.bar, 0);
+    return;
+  }
+  const int off = warp * kSpan * kRowBytes + lane * 4;
+  uint8_t *px = tx + off, *pg = tg + off, *pd = td + off;
+  {
+    float P[V], h[V], e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) P[i] = 1.f, h[i] = e[i] = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < kSpan; ++s) {
+      float g[V], x[V], dy[V];
+      gates<T>(pg + s * kRowBytes, starts, s, g);
+      read4(px + s * kRowBytes, x);
+      read4(pd + s * kRowBytes, dy);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[i] = decay_fma(g[i], h[i], x[i]);
+        P[i] *= g[i];
+        e[i] = P[i] == 0.f ? e[i] : fmaf(P[i], dy[i], e[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      sm.map[warp][f + i] = make_float2(P[i], h[i]);
+      sm.back[warp][f + i] = make_float2(P[i], e[i]);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float A[V], m[V], e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 1.f, m[i] = 0.f;
+    fold<V, F>(sm.back, f, kWarps - 1, -1, -1, A, m);
+    const bool ok = hand_off<V>(a, t, d, d < a.D, A, m, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sm.enter_back[f + i] = e[i];
+    if (lane == 0) sm.ok = ok;
+  }
+  // meanwhile: the states of this span
+  float A[V], h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = h0[i], A[i] = 1.f;
+  fold<V, F>(sm.map, f, 0, warp, 1, A, h);
+  float before[kSpan][V];
+#pragma unroll
+  for (int s = 0; s < kSpan; ++s) {
+    float g[V], x[V];
+    gates<T>(pg + s * kRowBytes, starts, s, g);
+    read4(px + s * kRowBytes, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      before[s][i] = h[i];
+      h[i] = decay_fma(g[i], h[i], x[i]);
+    }
+  }
+  __syncthreads();
+  if (!sm.ok) return;
+  float e[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) e[i] = sm.enter_back[f + i];
+  fold<V, F>(sm.back, f, kWarps - 1, warp, -1, A, e);
+#pragma unroll
+  for (int s = kSpan - 1; s >= 0; --s) {
+    float g[V], dh[V], dg[V];
+    gates<T>(pg + s * kRowBytes, starts, s, g);
+    read4(pd + s * kRowBytes, dh);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dh[i] += e[i];
+      e[i] = g[i] == 0.f ? 0.f : g[i] * dh[i];
+      dg[i] = g[i] == 0.f ? 0.f : e[i] * before[s][i];
+    }
+    write4(pd + s * kRowBytes, dh);   // dx over dy, dlog_a over log_a
+    write4(pg + s * kRowBytes, dg);
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    tma_store_3d(&mdx, td, t.tile * F, (int)t0, t.b);
+    tma_store_3d(&mdg, tg, t.tile * F, (int)t0, t.b);
+    bulk_commit();
+    bulk_wait_read_all();
+  }
 }
 
-__global__ void scan_bwd_carry_kernel(const float2* agg, const float* dstate_out, float* enter, float* dstate_in,
-                                      int64_t B, int64_t C, int64_t D) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= B * D) return;
-  const int64_t b = i / D, d = i % D;
-  float e = dstate_out ? dstate_out[i] : 0.f;
-  for (int64_t c = C - 1; c >= 0; --c) {
-    const int64_t j = (b * C + c) * D + d;
-    enter[j] = e;
-    e = decay_fma(agg[j].x, e, agg[j].y);
-  }
-  if (dstate_in) dstate_in[i] = e;
+// ------------------------------------------------------------------- host --
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(p)
+               : nullptr;
+  }();
+  return fn;
 }
 
-// One chunk's gradients: the states h_{t-1} again from the chunk's entering
-// state (kept in shared memory), then the reverse recurrence.
+// [B, L, D] as a 3D map {D, L, B}, box {128 bytes of features, 256, 1}.
 template <typename T>
-__global__ void __launch_bounds__(32) scan_bwd_out_kernel(const T* x, const T* log_a, const T* dy,
-                                                          const uint8_t* reset, const float* chunk_state,
-                                                          const float* enter, T* dx, T* dlog_a, int64_t L, int64_t D) {
-  __shared__ float hs[kScanChunk][32];
-  const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
-  if (d >= D) return;
-  const int64_t b = blockIdx.z, c = blockIdx.y;
-  const int64_t t0 = c * kScanChunk, t1 = min(L, t0 + kScanChunk);
-  float h = chunk_state[(b * gridDim.y + c) * D + d];
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t i = (b * L + t) * D + d;
-    const float a = decay_of(to_f32(log_a[i]), reset && reset[b * L + t]);
-    hs[t - t0][threadIdx.x] = h;
-    h = decay_fma(a, h, to_f32(x[i]));
+bool make_map(CUtensorMap* m, const void* base, const ScanProblem& p) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  constexpr cuuint64_t e = sizeof(T);
+  cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.L, (cuuint64_t)p.B};
+  cuuint64_t strides[2] = {(cuuint64_t)p.D * e, (cuuint64_t)p.L * p.D * e};
+  cuuint32_t box[3] = {kFT<T>, kScanChunk, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, e == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int64_t tiles_of(int64_t D, int dtype) {
+  const int64_t ft = dtype == kBF16 ? kFT<__nv_bfloat16> : kFT<float>;
+  return (D + ft - 1) / ft;
+}
+size_t sync_bytes(int64_t B, int64_t L, int64_t D, int dtype) {
+  return up256(sizeof(int) * (2 + (size_t)(B * tiles_of(D, dtype) * scan_chunks(L))));
+}
+int64_t groups_of(int64_t L) { return (scan_chunks(L) + kGroup - 1) / kGroup; }
+
+// Fill the arguments, enter and leave being the states at the walk's ends, and
+// clear the hand-off's flags.  The last chunk may be done before others of the
+// first group have read the entering state, so if it is to be overwritten
+// they read a copy (in the slot of the first group's state).
+cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, ScanArgs* a, cudaStream_t st) {
+  a->reset = p.reset;
+  a->chunk_state = p.chunk_state;
+  a->L = p.L;
+  a->D = p.D;
+  a->B = (int)p.B;
+  a->C = (int)scan_chunks(p.L);
+  a->tiles = (int)tiles_of(p.D, p.dtype);
+  a->status = p.status;
+  char* ws = static_cast<char*>(p.ws);
+  a->sync = reinterpret_cast<int*>(ws);
+  const size_t sb = sync_bytes(p.B, p.L, p.D, p.dtype);
+  a->map = reinterpret_cast<float2*>(ws + sb);
+  a->group = reinterpret_cast<float*>(ws + sb + up256(sizeof(float2) * p.B * a->C * p.D));
+  a->enter0 = enter;
+  a->enter0_stride = p.D;
+  a->leave = leave;
+  if (a->C == 1) return cudaSuccess;
+  if (enter && enter == leave) {
+    a->enter0 = a->group;
+    a->enter0_stride = groups_of(p.L) * p.D;
+    const size_t row = sizeof(float) * p.D;
+    if (cudaError_t e = cudaMemcpy2DAsync(a->group, row * groups_of(p.L), enter, row, row, p.B,
+                                          cudaMemcpyDeviceToDevice, st))
+      return e;
   }
-  float e = enter[(b * gridDim.y + c) * D + d];
-  for (int64_t t = t1 - 1; t >= t0; --t) {
-    const int64_t i = (b * L + t) * D + d;
-    const float a = decay_of(to_f32(log_a[i]), reset && reset[b * L + t]);
-    const float dh = to_f32(dy[i]) + e;
-    e = a == 0.f ? 0.f : a * dh;
-    dx[i] = from_f32<T>(dh);
-    dlog_a[i] = from_f32<T>(a == 0.f ? 0.f : e * hs[t - t0][threadIdx.x]);
-  }
+  return cudaMemsetAsync(ws, 0, sb, st);
 }
 
 template <typename T>
 cudaError_t scan_impl(const ScanProblem& p, cudaStream_t st) {
-  const int64_t C = scan_chunks(p.L);
-  float2* agg = static_cast<float2*>(p.ws);
-  float* enter = p.chunk_state ? p.chunk_state : reinterpret_cast<float*>(agg + p.B * C * p.D);
-  const dim3 grid((unsigned)((p.D + 127) / 128), (unsigned)C, (unsigned)p.B);
-  const T *x = static_cast<const T*>(p.x), *g = static_cast<const T*>(p.log_a);
-  scan_local_kernel<T><<<grid, 128, 0, st>>>(x, g, p.reset, agg, p.L, p.D);
-  scan_carry_kernel<<<(unsigned)((p.B * p.D + 127) / 128), 128, 0, st>>>(agg, p.state_in, enter, p.state_out, p.B, C,
-                                                                         p.D);
-  scan_out_kernel<T><<<grid, 128, 0, st>>>(x, g, p.reset, enter, static_cast<T*>(p.y), p.L, p.D);
+  CUtensorMap mx, mg, my;
+  if (!make_map<T>(&mx, p.x, p) || !make_map<T>(&mg, p.log_a, p) || !make_map<T>(&my, p.y, p))
+    return cudaErrorInvalidValue;
+  ScanArgs a;
+  cudaError_t e;
+  if ((e = set_args(p, p.state_in, p.state_out, &a, st))) return e;
+  constexpr int smem = 2 * kTileBytes + 128;
+  if ((e = cudaFuncSetAttribute(scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+  scan_kernel<T><<<(unsigned)(a.C * a.B * a.tiles), kThreads, smem, st>>>(mx, mg, my, a);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t scan_bwd_impl(const ScanProblem& p, cudaStream_t st) {
-  const int64_t C = scan_chunks(p.L);
-  float2* agg = static_cast<float2*>(p.ws);
-  float* enter = reinterpret_cast<float*>(agg + p.B * C * p.D);
-  const T *x = static_cast<const T*>(p.x), *g = static_cast<const T*>(p.log_a), *dy = static_cast<const T*>(p.dy);
-  const dim3 grid((unsigned)((p.D + 127) / 128), (unsigned)C, (unsigned)p.B);
-  scan_bwd_local_kernel<T><<<grid, 128, 0, st>>>(dy, g, p.reset, agg, p.L, p.D);
-  scan_bwd_carry_kernel<<<(unsigned)((p.B * p.D + 127) / 128), 128, 0, st>>>(agg, p.dstate_out, enter, p.dstate_in,
-                                                                             p.B, C, p.D);
-  const dim3 grid32((unsigned)((p.D + 31) / 32), (unsigned)C, (unsigned)p.B);
-  scan_bwd_out_kernel<T><<<grid32, 32, 0, st>>>(x, g, dy, p.reset, p.chunk_state, enter, static_cast<T*>(p.dx),
-                                                static_cast<T*>(p.dlog_a), p.L, p.D);
+  CUtensorMap mx, mg, mdy, mdx, mdg;
+  if (!make_map<T>(&mx, p.x, p) || !make_map<T>(&mg, p.log_a, p) || !make_map<T>(&mdy, p.dy, p) ||
+      !make_map<T>(&mdx, p.dx, p) || !make_map<T>(&mdg, p.dlog_a, p))
+    return cudaErrorInvalidValue;
+  ScanArgs a;
+  cudaError_t e;
+  if ((e = set_args(p, p.dstate_out, p.dstate_in, &a, st))) return e;
+  constexpr int smem = 3 * kTileBytes + 128;
+  if ((e = cudaFuncSetAttribute(scan_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+  scan_bwd_kernel<T><<<(unsigned)(a.C * a.B * a.tiles), kThreads, smem, st>>>(mx, mg, mdy, mdx, mdg, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int, bool) {
-  return (size_t)(B * scan_chunks(L) * D) * (sizeof(float2) + sizeof(float));
+bool scan_grid_fits(int64_t B, int64_t L, int64_t D, int dtype) {
+  // one block per tile; a tensor map's strides stay below 2^40 bytes
+  return (long double)B * tiles_of(D, dtype) * scan_chunks(L) < 2147483647.0L && (long double)L * D < 2.0e11L;
+}
+
+size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype, bool) {
+  if (scan_chunks(L) == 1) return 0;
+  return sync_bytes(B, L, D, dtype) + up256(sizeof(float2) * (size_t)(B * scan_chunks(L) * D)) +
+         up256(sizeof(float) * (size_t)(B * groups_of(L) * D));
 }
 
 cudaError_t launch_scan(const ScanProblem& p, cudaStream_t st) {
