@@ -431,7 +431,7 @@ int gecko_gated_scan_backward(const void* x, const void* log_a, const void* dy, 
 int gecko_qk_forward(const void* z, const float* scale, const float* shift, const int64_t* pos, void* q, void* k,
                      void* qm, void* km, int64_t B, int64_t T, int64_t H, int64_t d, float eps, int64_t pos0,
                      int64_t rot_dim, double rot_base, int interleaved, int dtype, void* stream);
-int gecko_qk_workspace(int64_t B, int64_t T, int64_t H, int64_t d, int64_t* bytes);   /* of the backward */
+int gecko_qk_workspace(int64_t B, int64_t T, int64_t H, int64_t d, int dtype, int64_t* bytes);   /* of the backward */
 int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, const void* dq, const void* dk,
                       const void* dqm, const void* dkm, void* dz, float* dscale, float* dshift, int64_t B,
                       int64_t T, int64_t H, int64_t d, float eps, int64_t pos0, int64_t rot_dim, double rot_base,

@@ -318,6 +318,46 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const __grid_constant
   }
 }
 
+// A few tokens (generation): no tile to fill, a thread walks over the tokens of
+// four features.  Measured, this takes 1.5 us + 0.23 us a token, the chunk
+// kernel 6.2 us + 0.014 us a tile (1 to 256 tokens of 512 to 131072 features).
+bool short_is_faster(int64_t L, int64_t tiles) { return L <= 128 && L <= 20 + tiles / 16; }
+
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T v[4];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(128) scan_short_kernel(const T* x, const T* log_a, T* y, const float* state_in,
+                                                         float* state_out, const ScanArgs a) {
+  const int64_t i = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 4;
+  if (i >= a.B * a.D) return;
+  const int64_t b = i / a.D, d = i - b * a.D;
+  float h[4] = {};
+  if (state_in) {
+    const float4 s = *reinterpret_cast<const float4*>(state_in + i);
+    h[0] = s.x, h[1] = s.y, h[2] = s.z, h[3] = s.w;
+  }
+  if (a.chunk_state) *reinterpret_cast<float4*>(a.chunk_state + i) = make_float4(h[0], h[1], h[2], h[3]);
+  const int64_t at = b * a.L * a.D + d;
+  const int L = (int)a.L;
+#pragma unroll 4
+  for (int t = 0; t < L; ++t) {
+    const Four<T> g = *reinterpret_cast<const Four<T>*>(log_a + at + t * a.D);
+    const Four<T> u = *reinterpret_cast<const Four<T>*>(x + at + t * a.D);
+    const bool start = a.reset && a.reset[b * a.L + t];
+    Four<T> o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = decay_fma(start ? 0.f : gate(to_f32(g.v[j]), T()), h[j], to_f32(u.v[j]));
+      o.v[j] = from_f32<T>(h[j]);
+    }
+    *reinterpret_cast<Four<T>*>(y + at + t * a.D) = o;
+  }
+  if (state_out) *reinterpret_cast<float4*>(state_out + i) = make_float4(h[0], h[1], h[2], h[3]);
+}
+
 // The backward walks the chunks from the last to the first.  A warp finds the
 // maps of both recurrences over its span in one ascending pass: with P_t the
 // product of the span's gates up to t, what the span passes back is
@@ -524,6 +564,17 @@ cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, Sca
 
 template <typename T>
 cudaError_t scan_impl(const ScanProblem& p, cudaStream_t st) {
+  if (short_is_faster(p.L, p.B * tiles_of(p.D, p.dtype))) {
+    ScanArgs a{};
+    a.reset = p.reset;
+    a.chunk_state = p.chunk_state;
+    a.L = p.L;
+    a.D = p.D;
+    a.B = (int)p.B;
+    scan_short_kernel<T><<<(unsigned)((p.B * p.D / 4 + 127) / 128), 128, 0, st>>>(
+        static_cast<const T*>(p.x), static_cast<const T*>(p.log_a), static_cast<T*>(p.y), p.state_in, p.state_out, a);
+    return cudaGetLastError();
+  }
   CUtensorMap mx, mg, my;
   if (!make_map<T>(&mx, p.x, p) || !make_map<T>(&mg, p.log_a, p) || !make_map<T>(&my, p.y, p))
     return cudaErrorInvalidValue;

@@ -100,7 +100,7 @@ def load() -> ctypes.CDLL:
             ("gated_scan_forward", [vp] * 7 + [i64] * 3 + [ci, vp, i64, vp]),
             ("gated_scan_backward", [vp] * 9 + [i64] * 3 + [ci, vp, i64, vp]),
             ("qk_forward", [vp] * 8 + [i64] * 4 + rot + [ci, vp]),
-            ("qk_workspace", [i64] * 4 + [out]),
+            ("qk_workspace", [i64] * 4 + [ci, out]),
             ("qk_backward", [vp] * 10 + [i64] * 4 + rot + [ci, vp, i64, vp]),
             ("linear_workspace", [i64] * 5 + [ci, ci, ci, out]),
             ("linear_forward", [vp] * 6 + [i64] * 5 + [ci, ci, vp, i64, vp]),
@@ -217,8 +217,8 @@ def gecko_qk_forward(z, scale, shift, pos, q, k, qm, km, B, T, H, d, eps, pos0, 
                                    interleaved, dtype, stream)
 
 
-def gecko_qk_workspace(B, T, H, d, bytes_out) -> int:
-    return load().gecko_qk_workspace(B, T, H, d, bytes_out)
+def gecko_qk_workspace(B, T, H, d, dtype, bytes_out) -> int:
+    return load().gecko_qk_workspace(B, T, H, d, dtype, bytes_out)
 
 
 def gecko_qk_backward(z, scale, pos, dq, dk, dqm, dkm, dz, dscale, dshift, B, T, H, d, eps, pos0, rot_dim, rot_base,
@@ -557,26 +557,30 @@ def _ptr(t) -> int:
 
 class _on:
     """The tensors' device and the call's stream as torch's current ones, so
-    that outputs and workspaces are allocated for the stream that uses them."""
+    that outputs and workspaces are allocated for the stream that uses them;
+    gives the stream's handle.  Nothing is switched that already is current."""
 
-    __slots__ = ("dev", "ctx")
+    __slots__ = ("dev", "ctx", "index")
 
     def __init__(self, device, stream):
         if stream is not None and stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.dev = torch.cuda.device(device)
+        self.index = device.index
+        self.dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
         self.ctx = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        self.dev.__enter__()
+        if self.dev is not None:
+            self.dev.__enter__()
         if self.ctx is not None:
             self.ctx.__enter__()
-        return int(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
-        return self.dev.__exit__(*exc)
+        if self.dev is not None:
+            self.dev.__exit__(*exc)
 
 
 def _workspace(query, args, device):
@@ -659,7 +663,7 @@ def qk_forward(z, scale, shift, eps: float = 1e-6, rot_dim: int = 0, rot_base: f
     dev = z.device
     _tensor(_required(shift, "shift"), "shift", (4, H, d), torch.float32, dev)
     with _on(dev, stream) as st:
-        outs = tuple(torch.empty((B, H, T, d), dtype=z.dtype, device=dev) for _ in range(4))
+        outs = tuple([z.new_empty((B, H, T, d)) for _ in range(4)])
         _check(gecko_qk_forward(z.data_ptr(), scale.data_ptr(), shift.data_ptr(), _ptr(pos),
                                 *(o.data_ptr() for o in outs), B, T, H, d, eps, pos0, rot_dim, rot_base,
                                 int(interleaved), _DT[z.dtype], st))
@@ -677,7 +681,7 @@ def qk_backward(z, scale, dq, dk, dqm, dkm, eps: float = 1e-6, rot_dim: int = 0,
         _tensor(_required(g, name), name, (B, H, T, d), z.dtype, dev)
     with _on(dev, stream) as st:
         dz, dscale, dshift = torch.empty_like(z), torch.empty_like(scale), torch.empty_like(scale)
-        ws, wp, wn = _workspace(gecko_qk_workspace, (B, T, H, d), dev)
+        ws, wp, wn = _workspace(gecko_qk_workspace, (B, T, H, d, _DT[z.dtype]), dev)
         _check(gecko_qk_backward(z.data_ptr(), scale.data_ptr(), _ptr(pos), *(g.data_ptr() for g in grads),
                                  dz.data_ptr(), dscale.data_ptr(), dshift.data_ptr(), B, T, H, d, eps, pos0, rot_dim,
                                  rot_base, int(interleaved), _DT[z.dtype], wp, wn, st))

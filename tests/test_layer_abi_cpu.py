@@ -113,9 +113,9 @@ def test_workspace_queries(so):
     n = ctypes.c_int64(-1)
     out = ctypes.byref(n)
     assert L.gecko_linear_workspace(2, 100, 64, 72, 0, 1, 1, 1, out) == 0 and n.value >= 2 * 200 * 64
-    assert L.gecko_qk_workspace(2, 100, 3, 64, out) == 0 and n.value >= 4 * 8 * 3 * 64
+    assert L.gecko_qk_workspace(2, 100, 3, 64, 1, out) == 0 and n.value >= 4 * 8 * 3 * 64
     assert L.gecko_gated_scan_workspace(2, 5000, 64, 1, 1, out) == 0 and n.value > 0
     assert L.gecko_linear_workspace(2, 100, 63, 72, 0, 1, 1, 1, out) == 2
-    assert L.gecko_qk_workspace(0, 100, 3, 64, out) == 1
+    assert L.gecko_qk_workspace(0, 100, 3, 64, 1, out) == 1
     assert L.gecko_gated_scan_workspace(2, 5000, 63, 1, 1, out) == 2
-    assert L.gecko_qk_workspace(2, 100, 3, 64, None) == 1
+    assert L.gecko_qk_workspace(2, 100, 3, 64, 1, None) == 1
