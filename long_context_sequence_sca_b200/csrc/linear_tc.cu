@@ -4,12 +4,12 @@
 // which covers x w^T, du w and du^T x without a transposed copy.
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
-// ring of stages, one thread issues tcgen05.mma, four warps empty the
+// ring of stages, one thread issues tcgen05.mma, eight warps empty the
 // accumulator (TMEM, two of them in turn) through shared memory, where they
-// transpose it so that every global access is a run of 128 bytes of one row.
-// With CG = 2 a pair of CTAs shares one 256 x BN tile: each loads its 128
+// transpose it so that every global access is a run of 64 bytes of one row.
+// With CG = 2 a pair of CTAs shares one 256 x kBN tile: each loads its 128
 // rows of A and half the rows of B, so a k-block moves half the bytes per
-// multiply-add of a 128 x BN tile; the even CTA issues the MMAs for both.
+// multiply-add of a 128 x kBN tile; the even CTA issues the MMAs for both.
 #include "common.cuh"
 #include "gecko_internal.h"
 #include "linear.cuh"
@@ -128,8 +128,10 @@ __device__ __forceinline__ void tmem_give(uint32_t taddr, uint32_t cols) {
 // ------------------------------------------------------------- work split --
 
 constexpr int kBK = 64;              // k-block: one 128-byte swizzle row
-constexpr int kGemmThreads = 256;    // TMA, MMA, TMEM, idle warp; four epilogue warps
-constexpr int kEpilogueWarp = 4;
+constexpr int kBN = 256;             // columns per tile
+constexpr int kGemmThreads = 384;    // TMA, MMA, TMEM, idle warp; eight epilogue warps
+constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8;
+constexpr int kBand = 32;            // columns an epilogue warp takes at a time
 constexpr int kGroupM = 8;           // tiles of one column band done together (operand reuse in L2)
 
 struct GemmShape {
@@ -158,42 +160,62 @@ __device__ __forceinline__ Unit unit_at(const GemmShape& g, int u) {
 
 // -------------------------------------------------------------- epilogues --
 
-// Each gives, for 8 consecutive columns n of row m, what is written.  Row and
-// column parts of an address are separate: rows are fixed for a tile.
+// Each writes 8 consecutive columns n of a row.  Row and column parts of an
+// address are separate: rows are fixed for a tile, columns for a band of it.
+// What has to be read (bias, residual) is fetched for a whole band before it
+// is used, so that its latency is paid once.
+
+struct None {};
 
 struct EpiForward {
   const float* bias;
   const __nv_bfloat16* residual;
   __nv_bfloat16 *y, *pre;
   int N, T, H, hd, act;
+  struct Band {
+    int64_t col;
+    float bias[8];
+  };
+  using Fetched = uint4;
   __device__ __forceinline__ int64_t row(int64_t m) const {
     if (H == 0) return m * N;
     const uint32_t b = (uint32_t)m / (uint32_t)T, t = (uint32_t)m - b * (uint32_t)T;
     return ((int64_t)b * H * T + t) * hd;
   }
-  __device__ __forceinline__ int64_t col(int n) const {
-    if (H == 0) return n;
-    const int h = n / hd;
-    return (int64_t)h * T * hd + (n - h * hd);
-  }
-  __device__ __forceinline__ void put(int64_t row, int64_t col, int n, int /*split*/, float (&v)[8]) const {
-    if (bias) {
-      float b[8];
-      load_f8(bias + n, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += b[i];
+  __device__ __forceinline__ Band band(int n) const {
+    Band c;
+    c.col = n;
+    if (H) {
+      const int h = n / hd;
+      c.col = (int64_t)h * T * hd + (n - h * hd);
     }
-    const int64_t at = row + col;
-    if (pre) store_f8(pre + at, v);
-    if (act != kActNone) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], act);
+    for (int i = 0; i < 8; ++i) c.bias[i] = 0.f;
+    if (bias) load_f8(bias + n, c.bias);
+    return c;
+  }
+  __device__ __forceinline__ Fetched fetch(int64_t row, const Band& c, bool on) const {
+    return residual && on ? *reinterpret_cast<const uint4*>(residual + row + c.col) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void put(int64_t row, const Band& c, int, const Fetched& f, float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += c.bias[i];
+    const int64_t at = row + c.col;
+    if (pre) store_f8(pre + at, v);
+    if (act == kActSilu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kActSilu);
+    } else if (act == kActGelu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kActGelu);
     }
     if (residual) {
-      float r[8];
-      load_f8(residual + at, r);
+      const uint32_t w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __uint_as_float(w[i] << 16);
+        v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
     store_f8(y + at, v);
   }
@@ -202,10 +224,13 @@ struct EpiForward {
 struct EpiPlain {
   __nv_bfloat16* c;
   int N;
+  using Band = int;
+  using Fetched = None;
   __device__ __forceinline__ int64_t row(int64_t m) const { return m * N; }
-  __device__ __forceinline__ int64_t col(int n) const { return n; }
-  __device__ __forceinline__ void put(int64_t row, int64_t col, int, int, float (&v)[8]) const {
-    store_f8(c + row + col, v);
+  __device__ __forceinline__ Band band(int n) const { return n; }
+  __device__ __forceinline__ Fetched fetch(int64_t, Band, bool) const { return {}; }
+  __device__ __forceinline__ void put(int64_t row, Band n, int, Fetched, float (&v)[8]) const {
+    store_f8(c + row + n, v);
   }
 };
 
@@ -213,19 +238,22 @@ struct EpiPartial {
   float* part;   // [splits, M, N]
   int64_t M;
   int N;
+  using Band = int;
+  using Fetched = None;
   __device__ __forceinline__ int64_t row(int64_t m) const { return m * N; }
-  __device__ __forceinline__ int64_t col(int n) const { return n; }
-  __device__ __forceinline__ void put(int64_t row, int64_t col, int, int split, float (&v)[8]) const {
-    store_f8(part + (int64_t)split * M * N + row + col, v);
+  __device__ __forceinline__ Band band(int n) const { return n; }
+  __device__ __forceinline__ Fetched fetch(int64_t, Band, bool) const { return {}; }
+  __device__ __forceinline__ void put(int64_t row, Band n, int split, Fetched, float (&v)[8]) const {
+    store_f8(part + (int64_t)split * M * N + row + n, v);
   }
 };
 
 // ----------------------------------------------------------------- kernel --
 
-template <int CG, int BN>
+template <int CG>
 struct GemmCfg {
-  static constexpr int kA = 128 * kBK * 2, kB = BN / CG * kBK * 2, kStage = kA + kB;
-  static constexpr int kStaging = 4 * 32 * 64 * 4;   // per epilogue warp: 32 rows x 64 columns, fp32
+  static constexpr int kA = 128 * kBK * 2, kB = kBN / CG * kBK * 2, kStage = kA + kB;
+  static constexpr int kStaging = kEpilogueWarps * 32 * kBand * 4;   // per warp: 32 rows x 32 columns, fp32
   static constexpr int kStages = (232448 - 1024 - 512 - kStaging) / kStage > 8
                                      ? 8 : (232448 - 1024 - 512 - kStaging) / kStage;
   static constexpr int kStageOff = kStages * kStage;
@@ -233,15 +261,15 @@ struct GemmCfg {
   static constexpr int kNumBars = 2 * kStages + 4;   // full, empty; accumulator full, empty
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
-  static constexpr uint32_t kTmemCols = 2 * BN;
+  static constexpr uint32_t kTmemCols = 2 * kBN;
   static_assert(kAlloc <= 232448, "shared memory above the per-block limit");
 };
 
-template <int CG, int BN, bool AMN, bool BMN, class Epi>
+template <int CG, bool AMN, bool BMN, class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_constant__ CUtensorMap ma,
                                                                   const __grid_constant__ CUtensorMap mb,
                                                                   const GemmShape g, const Epi ep, int* status) {
-  using Cfg = GemmCfg<CG, BN>;
+  using Cfg = GemmCfg<CG>;
   constexpr int NS = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -264,10 +292,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 4 * CG);
+      mbar_init(acc_empty + i, kEpilogueWarps * CG);
     }
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (warp == 3 && lane == 0) {
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mb);
   }
   if (warp == 2) tmem_take<CG>(tmem_slot, Cfg::kTmemCols);
   tc_fence_before();
@@ -283,7 +315,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
       bool ok = true;
       for (int u = first; u < units && ok; u += step) {
         const Unit t = unit_at(g, u);
-        const int m0 = (t.m * CG + (int)rank) * 128, n0 = t.n * BN + (int)rank * (BN / CG);
+        const int m0 = (t.m * CG + (int)rank) * 128, n0 = t.n * kBN + (int)rank * (kBN / CG);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % NS;
           if (it >= NS && !(ok = mbar_wait_cluster(empty + s, (it / NS - 1) & 1, abort_flag, status))) break;
@@ -298,7 +330,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
           }
           if (BMN) {
 #pragma unroll
-            for (int i = 0; i < BN / CG / 64; ++i) tma_load<CG>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK);
+            for (int i = 0; i < kBN / CG / 64; ++i) tma_load<CG>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK);
           } else {
             tma_load<CG>(pb, &mb, bar, kb * kBK, n0);
           }
@@ -318,7 +350,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer --
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128 * CG, BN, AMN, BMN);
+      constexpr uint32_t idesc = idesc_bf16_f32(128 * CG, kBN, AMN, BMN);
       const uint32_t base = smem_u32(smem);
       int it = 0, k = 0;
       bool ok = true;
@@ -336,7 +368,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
           const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
-            umma<CG>(tmem + acc * BN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
+            umma<CG>(tmem + acc * kBN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
                      idesc, kb > t.kb0 || kk > 0 ? 1u : 0u);
           umma_done<CG>(empty + s);
         }
@@ -346,55 +378,69 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
     __syncwarp();
   } else if (warp >= kEpilogueWarp) {
     // ----------------------------------------------------------- epilogue --
-    const int q = warp - kEpilogueWarp;   // TMEM lane quarter (warp % 4)
-    float* stage = reinterpret_cast<float*>(smem + Cfg::kStageOff) + q * 32 * 64;
-    const int c8 = lane % 8, r4 = lane / 8;
+    const int q = warp % 4;   // the TMEM lanes a warp may read: rows 32 q ..
+    float* stage = reinterpret_cast<float*>(smem + Cfg::kStageOff) + (warp - kEpilogueWarp) * 32 * kBand;
+    // Reading back, 4 lanes share a row and 8 lanes a conflict-free access:
+    // rows r and r + 4.
+    const int c4 = lane % 4, r8 = (lane >> 3) | ((lane & 4) ? 4 : 0);
+    const int first_band = (warp - kEpilogueWarp) / 4;   // two warps per row quarter take bands in turn
     int k = 0;
     bool ok = true;
     for (int u = first; u < units; u += step, ++k) {
       const Unit t = unit_at(g, u);
       const int acc = k & 1;
+      const int64_t m0 = ((int64_t)t.m * CG + rank) * 128 + q * 32 + r8;
+      const int n0 = t.n * kBN + c4 * 8;
+      int64_t row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i] = ep.row(m0 + 8 * i);
+      // bias and residual of a band, fetched one band ahead
+      typename Epi::Band band{};
+      typename Epi::Fetched fetched[4];
+      auto fetch = [&](int c) {
+        const int n = n0 + c * kBand;
+        if (c < kBN / kBand && n < g.N) {
+          band = ep.band(n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) fetched[i] = ep.fetch(row[i], band, m0 + 8 * i < g.M);
+        }
+      };
+      fetch(first_band);
       ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full + acc, (k / 2) & 1, abort_flag, status));
       if (!ok) break;
       tc_fence_after();
-      const int64_t m0 = ((int64_t)t.m * CG + rank) * 128 + q * 32;
-      const int n0 = t.n * BN;
-      int64_t row[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) row[i] = ep.row(m0 + 4 * i + r4);
-      const uint32_t from = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
+      const uint32_t from = tmem + acc * kBN + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN / 64; ++c) {
-        uint32_t v[64];
-        tmem_ld32p(from + c * 64, v);
-        tmem_ld32p(from + c * 64 + 32, v + 32);
+      for (int c = first_band; c < kBN / kBand; c += 2) {
+        uint32_t v[32];
+        tmem_ld32p(from + c * kBand, v);
         tmem_wait_ld();
-        if (c == BN / 64 - 1) {
+        if (c + 2 >= kBN / kBand) {
           // the accumulator is read: the MMAs of the unit after next may write it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(CG == 1 ? smem_u32(acc_empty + acc) : map_to(acc_empty + acc, 0));
         }
         // lane = row; 16-byte piece j of a row lies at (even pieces, then odd) ^ row: no bank conflicts
-        // here, nor below where 8 lanes read one row
+        // here, nor below
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((((j >> 1) | ((j & 1) << 3)) ^ (lane & 7)) << 2)) =
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(stage + lane * kBand + ((((j >> 1) | ((j & 1) << 2)) ^ (lane & 7)) << 2)) =
               make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         __syncwarp();
-        const int n = n0 + c * 64 + c8 * 8;
-        if (n < g.N) {
-          const int64_t col = ep.col(n);
+        const typename Epi::Band b = band;
+        typename Epi::Fetched f[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + r4;
-            if (m0 + r < g.M) {
-              const float* p = stage + r * 64;
-              const float4 lo = *reinterpret_cast<const float4*>(p + ((c8 ^ (r & 7)) << 2));
-              const float4 hi = *reinterpret_cast<const float4*>(p + (((c8 + 8) ^ (r & 7)) << 2));
-              float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-              ep.put(row[i], col, n, t.split, w);
-            }
+        for (int i = 0; i < 4; ++i) f[i] = fetched[i];
+        fetch(c + 2);
+        if (n0 + c * kBand < g.N) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* p = stage + (8 * i + r8) * kBand;
+            const float4 lo = *reinterpret_cast<const float4*>(p + ((c4 ^ r8) << 2));
+            const float4 hi = *reinterpret_cast<const float4*>(p + (((c4 + 4) ^ r8) << 2));
+            float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (m0 + 8 * i < g.M) ep.put(row[i], b, t.split, f[i], w);
           }
         }
         __syncwarp();
@@ -423,7 +469,9 @@ __global__ void __launch_bounds__(256) gemm_sum_kernel(const float* part, int sp
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += w[j];
   }
-  ep.put(ep.row(m), ep.col(n), n, 0, v);
+  const typename Epi::Band band = ep.band(n);
+  const int64_t row = ep.row(m);
+  ep.put(row, band, 0, ep.fetch(row, band, true), v);
 }
 
 // ------------------------------------------------------------------- host --
@@ -465,43 +513,38 @@ struct Operand {
 };
 
 struct GemmPlan {
-  int cg, bn;
+  int cg;
   GemmShape g;
 };
 
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K) {
   GemmPlan pl;
-  pl.cg = 2;
-  pl.bn = 256;
-  auto tiles = [&](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
-  if ((int64_t)tiles(M, 256) * tiles(N, 256) < sm_count() / 2) {
-    pl.cg = 1;
-    pl.bn = 128;
-  }
+  auto tiles = [](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
+  pl.cg = M <= 128 ? 1 : 2;
   pl.g.M = M;
   pl.g.N = N;
   pl.g.tiles_m = tiles(M, 128 * pl.cg);
-  pl.g.tiles_n = tiles(N, pl.bn);
+  pl.g.tiles_n = tiles(N, kBN);
   pl.g.k_blocks = tiles(K, kBK);
-  const int slots = sm_count() / pl.cg, t = pl.g.tiles_m * pl.g.tiles_n;
-  int splits = slots / t;
+  const int64_t slots = sm_count() / pl.cg, t = (int64_t)pl.g.tiles_m * pl.g.tiles_n;
+  int64_t splits = pl.g.k_blocks < 32 ? 1 : slots / t;
   if (splits > pl.g.k_blocks / 8) splits = pl.g.k_blocks / 8;
   if (splits < 1) splits = 1;
-  pl.g.blocks_per_split = (pl.g.k_blocks + splits - 1) / splits;
+  pl.g.blocks_per_split = (int)((pl.g.k_blocks + splits - 1) / splits);
   pl.g.splits = (pl.g.k_blocks + pl.g.blocks_per_split - 1) / pl.g.blocks_per_split;
   return pl;
 }
 
-template <int CG, int BN, bool AMN, bool BMN, class Epi>
+template <int CG, bool AMN, bool BMN, class Epi>
 cudaError_t run_gemm(const GemmPlan& pl, const Operand& A, const Operand& B, int64_t K, const Epi& ep, int* status,
                      cudaStream_t st) {
-  using Cfg = GemmCfg<CG, BN>;
+  using Cfg = GemmCfg<CG>;
   CUtensorMap ma, mb;
   cudaError_t e;
   const GemmShape& g = pl.g;
   if ((e = AMN ? make_map(&ma, A.p, K, g.M, kBK) : make_map(&ma, A.p, g.M, K, 128))) return e;
-  if ((e = BMN ? make_map(&mb, B.p, K, g.N, kBK) : make_map(&mb, B.p, g.N, K, BN / CG))) return e;
-  auto kern = gemm_tc_kernel<CG, BN, AMN, BMN, Epi>;
+  if ((e = BMN ? make_map(&mb, B.p, K, g.N, kBK) : make_map(&mb, B.p, g.N, K, kBN / CG))) return e;
+  auto kern = gemm_tc_kernel<CG, AMN, BMN, Epi>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kAlloc))) return e;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
   const int64_t slots = sm_count() / CG;
@@ -522,8 +565,8 @@ cudaError_t run_gemm(const GemmPlan& pl, const Operand& A, const Operand& B, int
 template <bool AMN, bool BMN, class Epi>
 cudaError_t gemm_of(const GemmPlan& pl, const Operand& A, const Operand& B, int64_t K, const Epi& ep, int* status,
                     cudaStream_t st) {
-  return pl.cg == 2 ? run_gemm<2, 256, AMN, BMN, Epi>(pl, A, B, K, ep, status, st)
-                    : run_gemm<1, 128, AMN, BMN, Epi>(pl, A, B, K, ep, status, st);
+  return pl.cg == 2 ? run_gemm<2, AMN, BMN, Epi>(pl, A, B, K, ep, status, st)
+                    : run_gemm<1, AMN, BMN, Epi>(pl, A, B, K, ep, status, st);
 }
 
 template <bool AMN, bool BMN, class Epi>
