@@ -95,33 +95,52 @@ void simt_gemm(const void* A, int64_t am, int64_t ak, const void* B, int64_t bn,
 // ----------------------------------------------------- gradient of u, db --
 
 constexpr int kDuCols = 256;     // columns per block: 32 threads x 8
-constexpr int kDuRowsPar = 8;    // rows in flight per block
+constexpr int kDuRowsPar = 8;    // rows per round of a block
+constexpr int kDuUnroll = 4;     // rounds whose loads are in flight together
+constexpr int kDuBlocks = 4;     // per SM
 
 // du = dy f'(u), [M, N] row-major in the tensors' type (one rounding, the
 // operand type of the two products that follow); the column sums of the
 // unrounded values go to part [gridDim.y, N].
-template <typename T>
-__global__ void __launch_bounds__(256) linear_du_kernel(const T* dy, const T* pre, T* du, float* part, OutLayout lay,
-                                                        int64_t M, int64_t N, int64_t rows, int act) {
+template <typename T, int kAct>
+__global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, const T* pre, T* du, float* part,
+                                                                   OutLayout lay, int64_t M, int64_t N, int64_t rows) {
   __shared__ float red[kDuRowsPar][kDuCols];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int64_t n = (int64_t)blockIdx.x * kDuCols + cx * 8;
   const int64_t m1 = min(M, ((int64_t)blockIdx.y + 1) * rows);
   float acc[8] = {};
-  if (n < N)
-    for (int64_t m = (int64_t)blockIdx.y * rows + ry; m < m1; m += kDuRowsPar) {
-      const int64_t at = lay.at(m, n);
-      float g[8], u[8];
-      load_f8(dy + at, g);
-      if (act != kActNone) {
-        load_f8(pre + at, u);
+  if (n < N) {
+    const int64_t col = lay.col((int)n);
+    for (int64_t m = (int64_t)blockIdx.y * rows + ry; m < m1; m += kDuRowsPar * kDuUnroll) {
+      Vec8<T> g[kDuUnroll], u[kDuUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= act_slope(u[i], act);
+      for (int i = 0; i < kDuUnroll; ++i) {
+        const int64_t mi = m + i * kDuRowsPar;
+        if (mi < m1) {
+          const int64_t at = lay.row(mi) + col;
+          g[i].load(dy + at);
+          if (kAct != kActNone) u[i].load(pre + at);
+        }
       }
-      if (du) store_f8(du + m * N + n, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += g[i];
+      for (int i = 0; i < kDuUnroll; ++i) {
+        const int64_t mi = m + i * kDuRowsPar;
+        if (mi < m1) {
+          float v[8], w[8];
+          g[i].get(v);
+          if (kAct != kActNone) {
+            u[i].get(w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= act_slope(w[j], kAct);
+          }
+          if (du) store_f8(du + mi * N + n, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += v[j];
+        }
+      }
     }
+  }
   if (!part) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[ry][cx * 8 + i] = acc[i];
@@ -154,12 +173,25 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int r
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Blocks of rows of the du pass.
+// Blocks of rows of the du pass: one wave, each with a few rounds at least.
 int64_t du_row_blocks(int64_t M, int64_t N) {
   const int64_t cols = (N + kDuCols - 1) / kDuCols;
-  int64_t blocks = (148 * 8 + cols - 1) / cols;
-  const int64_t most = (M + 4 * kDuRowsPar - 1) / (4 * kDuRowsPar);
+  int64_t blocks = (int64_t)kDuBlocks * sm_count() / cols;
+  if (blocks < 1) blocks = 1;
+  if (blocks > 65535) blocks = 65535;
+  const int64_t most = (M + kDuUnroll * kDuRowsPar - 1) / (kDuUnroll * kDuRowsPar);
   return blocks < most ? blocks : most;
+}
+
+template <typename T>
+void launch_du(const LinearProblem& p, T* du, float* part, int64_t blocks, cudaStream_t st) {
+  const dim3 grid((unsigned)((p.N + kDuCols - 1) / kDuCols), (unsigned)blocks);
+  const int64_t rows = (p.M() + blocks - 1) / blocks;
+  const T *dy = static_cast<const T*>(p.dy), *pre = static_cast<const T*>(p.pre);
+  const OutLayout lay(p);
+  if (p.act == kActNone) linear_du_kernel<T, kActNone><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+  else if (p.act == kActSilu) linear_du_kernel<T, kActSilu><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+  else linear_du_kernel<T, kActGelu><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
 }
 
 // Whether dy itself is du, laid out as the products need it.
@@ -192,11 +224,8 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   float* part = reinterpret_cast<float*>(ws + du_bytes(p));
   const bool products = p.dx || p.dw;
   if (p.db || (!alias && products)) {
-    const int64_t blocks = du_row_blocks(M, p.N), rows = (M + blocks - 1) / blocks;
-    const dim3 grid((unsigned)((p.N + kDuCols - 1) / kDuCols), (unsigned)blocks);
-    linear_du_kernel<T><<<grid, 256, 0, st>>>(static_cast<const T*>(p.dy), static_cast<const T*>(p.pre),
-                                              products ? du : nullptr, p.db ? part : nullptr, OutLayout(p), M, p.N,
-                                              rows, p.act);
+    const int64_t blocks = du_row_blocks(M, p.N);
+    launch_du<T>(p, products ? du : nullptr, p.db ? part : nullptr, blocks, st);
     if (p.db)
       linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
   }

@@ -171,24 +171,17 @@ struct EpiForward {
   const float* bias;
   const __nv_bfloat16* residual;
   __nv_bfloat16 *y, *pre;
-  int N, T, H, hd, act;
+  OutLayout lay;
+  int act;
   struct Band {
     int64_t col;
     float bias[8];
   };
   using Fetched = uint4;
-  __device__ __forceinline__ int64_t row(int64_t m) const {
-    if (H == 0) return m * N;
-    const uint32_t b = (uint32_t)m / (uint32_t)T, t = (uint32_t)m - b * (uint32_t)T;
-    return ((int64_t)b * H * T + t) * hd;
-  }
+  __device__ __forceinline__ int64_t row(int64_t m) const { return lay.row(m); }
   __device__ __forceinline__ Band band(int n) const {
     Band c;
-    c.col = n;
-    if (H) {
-      const int h = n / hd;
-      c.col = (int64_t)h * T * hd + (n - h * hd);
-    }
+    c.col = lay.col(n);
 #pragma unroll
     for (int i = 0; i < 8; ++i) c.bias[i] = 0.f;
     if (bias) load_f8(bias + n, c.bias);
@@ -589,9 +582,12 @@ size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K) {
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, cudaStream_t st) {
-  const EpiForward ep{p.bias,   static_cast<const __nv_bfloat16*>(p.residual),
-                      static_cast<__nv_bfloat16*>(p.y), static_cast<__nv_bfloat16*>(p.pre),
-                      (int)p.N, (int)p.T, (int)p.H, p.H ? (int)(p.N / p.H) : 1, p.act};
+  const EpiForward ep{p.bias,
+                      static_cast<const __nv_bfloat16*>(p.residual),
+                      static_cast<__nv_bfloat16*>(p.y),
+                      static_cast<__nv_bfloat16*>(p.pre),
+                      OutLayout(p),
+                      p.act};
   return gemm<false, false>(p.M(), p.N, p.K, p.x, p.w, ep, p.ws, p.status, st);
 }
 

@@ -7,6 +7,7 @@ is no fallback: if the library is missing or cannot load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -533,7 +534,7 @@ ACTS = {"none": 0, "silu": 1, "gelu": 2}
 
 def _tensor(t, name, shape, dtype, device):
     """Check one argument; None stays None."""
-    if t is not None and not (isinstance(t, torch.Tensor) and t.is_contiguous() and tuple(t.shape) == shape
+    if t is not None and not (isinstance(t, torch.Tensor) and t.is_contiguous() and t.shape == shape
                               and t.dtype == dtype and t.device == device):
         raise ValueError(f"{name} must be a contiguous {shape} {dtype} tensor on {device}")
     return t
@@ -583,14 +584,21 @@ class _on:
             self.dev.__exit__(*exc)
 
 
-def _workspace(query, args, device):
-    """(tensor or None, pointer, bytes) of a call's working memory."""
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(query, *args) -> int:
+    """The bytes a call of these sizes needs (a function of the sizes alone)."""
     n = ctypes.c_int64(0)
     _check(query(*args, ctypes.byref(n)))
-    if n.value == 0:
+    return n.value
+
+
+def _workspace(query, args, device):
+    """(tensor or None, pointer, bytes) of a call's working memory."""
+    n = _workspace_bytes(query, *args)
+    if n == 0:
         return None, 0, 0
-    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
-    return ws, ws.data_ptr(), n.value
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), n
 
 
 def gated_scan_forward(x, log_a, reset=None, state_in=None, return_state=False, keep_chunks=False, y=None,
