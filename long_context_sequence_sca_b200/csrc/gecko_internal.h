@@ -289,11 +289,12 @@ struct LinearProblem {
 size_t linear_workspace_bytes(const LinearProblem& p, bool backward);
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st);
 cudaError_t launch_linear_bwd(const LinearProblem& p, cudaStream_t st);
-// Tensor-core (tcgen05) products, bf16.  ws: gemm_tc_workspace of the
-// product's rows, columns and depth.
-size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K);
-cudaError_t launch_linear_tc(const LinearProblem& p, cudaStream_t st);
-cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, void* ws, cudaStream_t st);
-cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, void* ws, cudaStream_t st);
+// Tensor-core (tcgen05) products.  The operands are p's, or du, for bf16; their
+// three bf16 planes for fp32.  ws: gemm_tc_workspace of the product's rows,
+// columns and depth.
+size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype);
+cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st);
+cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, const void* w, void* ws, cudaStream_t st);
+cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, const void* x, void* ws, cudaStream_t st);
 
 }  // namespace gecko

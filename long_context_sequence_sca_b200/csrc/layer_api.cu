@@ -180,7 +180,7 @@ int check_linear_sizes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, in
   if (H && (N % H || (N / H) % 8))
     return fail(GECKO_ERR_SHAPE, "N / H must be a multiple of 8 (N=%lld H=%lld)", (long long)N, (long long)H);
   const int64_t most = (int64_t(1) << 31) - 256, wide = int64_t(1) << 20;
-  if (B > most || T > most || B * T > most || N > wide || K > wide)
+  if (B > most || T > most || B * T > most || N > wide || K > wide || B * T * (N > K ? N : K) > int64_t(1) << 38)
     return fail(GECKO_ERR_SHAPE, "B * T, N or K exceeds the kernels' range (B=%lld T=%lld N=%lld K=%lld)",
                 (long long)B, (long long)T, (long long)N, (long long)K);
   return GECKO_OK;

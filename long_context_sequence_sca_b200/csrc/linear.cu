@@ -1,9 +1,10 @@
 // Projection y = f(x w^T + bias) + residual and its gradients:
 //   u = x w^T + bias,  du = dy (.) f'(u),
 //   dx = du w,  dw = du^T x,  db = column sums of du.
-// The kernels here are CUDA-core ones: the products for fp32 (and for bf16
-// under GECKO_KERNELS=simt), and the pass that forms du and db.  The bf16
-// products run on the tensor cores (linear_tc.cu).
+// The products run on the tensor cores (linear_tc.cu); here are the pass that
+// forms du and db, the pass that splits fp32 operands into bf16 planes, and
+// CUDA-core products for GECKO_KERNELS=simt, a second implementation to check
+// against.
 #include <cstdlib>
 #include <cstring>
 
@@ -99,11 +100,11 @@ constexpr int kDuRowsPar = 8;    // rows per round of a block
 constexpr int kDuUnroll = 4;     // rounds whose loads are in flight together
 constexpr int kDuBlocks = 4;     // per SM
 
-// du = dy f'(u), [M, N] row-major in the tensors' type (one rounding, the
-// operand type of the two products that follow); the column sums of the
-// unrounded values go to part [gridDim.y, N].
-template <typename T, int kAct>
-__global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, const T* pre, T* du, float* part,
+// du = dy f'(u), [M, N] row-major in the tensors' type (for bf16 one rounding, to
+// the operand type of the two products that follow) or as bf16 planes; the
+// column sums of the unrounded values go to part [gridDim.y, N].
+template <typename T, int kAct, bool kPlanes>
+__global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, const T* pre, void* du, float* part,
                                                                    OutLayout lay, int64_t M, int64_t N, int64_t rows) {
   __shared__ float red[kDuRowsPar][kDuCols];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -134,7 +135,10 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= act_slope(w[j], kAct);
           }
-          if (du) store_f8(du + mi * N + n, v);
+          if (du) {
+            if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + mi * N + n, M * N, v);
+            else store_f8(static_cast<T*>(du) + mi * N + n, v);
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] += v[j];
         }
@@ -183,81 +187,130 @@ int64_t du_row_blocks(int64_t M, int64_t N) {
   return blocks < most ? blocks : most;
 }
 
-template <typename T>
-void launch_du(const LinearProblem& p, T* du, float* part, int64_t blocks, cudaStream_t st) {
+template <typename T, bool kPlanes>
+void launch_du(const LinearProblem& p, void* du, float* part, int64_t blocks, cudaStream_t st) {
   const dim3 grid((unsigned)((p.N + kDuCols - 1) / kDuCols), (unsigned)blocks);
   const int64_t rows = (p.M() + blocks - 1) / blocks;
   const T *dy = static_cast<const T*>(p.dy), *pre = static_cast<const T*>(p.pre);
   const OutLayout lay(p);
-  if (p.act == kActNone) linear_du_kernel<T, kActNone><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
-  else if (p.act == kActSilu) linear_du_kernel<T, kActSilu><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
-  else linear_du_kernel<T, kActGelu><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+  if (p.act == kActNone)
+    linear_du_kernel<T, kActNone, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+  else if (p.act == kActSilu)
+    linear_du_kernel<T, kActSilu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+  else
+    linear_du_kernel<T, kActGelu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
 }
 
-// Whether dy itself is du, laid out as the products need it.
-bool dy_is_du(const LinearProblem& p) { return p.act == kActNone && p.H == 0; }
+// The bf16 planes of n fp32 values (n a multiple of 8).
+__global__ void __launch_bounds__(256) split_kernel(const float* v, __nv_bfloat16* planes, int64_t n) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float w[8];
+  load_f8(v + i, w);
+  store_planes(planes + i, n, w);
+}
 
-size_t du_bytes(const LinearProblem& p) {
-  return dy_is_du(p) ? 0 : up256((p.dtype == kBF16 ? 2 : 4) * (size_t)p.M() * p.N);
+void launch_split(const void* v, void* planes, int64_t n, cudaStream_t st) {
+  split_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, st>>>(static_cast<const float*>(v),
+                                                               static_cast<__nv_bfloat16*>(planes), n);
 }
 
 // GECKO_KERNELS=simt selects the CUDA-core kernels for every type.
-bool use_tc(const LinearProblem& p) {
+bool use_tc() {
   const char* e = std::getenv("GECKO_KERNELS");
-  return p.dtype == kBF16 && !(e && std::strcmp(e, "simt") == 0);
+  return !(e && std::strcmp(e, "simt") == 0);
+}
+
+// Where the working memory's parts lie.  The CUDA-core path uses du, as the
+// tensors' type, and part.
+struct Layout {
+  bool dy_is_du;       // dy is already laid out as the products need it
+  size_t du, part, x, w, gemm, bytes;
+};
+
+size_t plane_bytes(int64_t n) { return up256(3 * sizeof(__nv_bfloat16) * (size_t)n); }
+
+Layout layout_of(const LinearProblem& p, bool backward) {
+  const int64_t M = p.M();
+  const bool f32 = p.dtype == kF32;
+  Layout l{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += up256(n);
+    return here;
+  };
+  l.dy_is_du = !f32 && p.act == kActNone && p.H == 0;
+  if (backward) {
+    // planes take more than the fp32 values
+    l.du = take(l.dy_is_du ? 0 : f32 ? plane_bytes(M * p.N) : 2 * (size_t)M * p.N);
+    l.part = take(sizeof(float) * du_row_blocks(M, p.N) * p.N);
+  }
+  l.x = take(f32 ? plane_bytes(M * p.K) : 0);
+  l.w = take(f32 ? plane_bytes(p.N * p.K) : 0);
+  size_t g = backward ? gemm_tc_workspace(M, p.K, p.N, p.dtype) : gemm_tc_workspace(M, p.N, p.K, p.dtype);
+  if (backward) {
+    const size_t dw = gemm_tc_workspace(p.N, p.K, M, p.dtype);
+    if (dw > g) g = dw;
+  }
+  l.gemm = take(g);
+  l.bytes = at;
+  return l;
 }
 
 template <typename T>
-cudaError_t forward_simt(const LinearProblem& p, cudaStream_t st) {
-  ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
-                   OutLayout(p), p.act};
-  simt_gemm<T>(p.x, p.K, 1, p.w, p.K, 1, p.M(), p.N, p.K, ep, st);
-  return cudaGetLastError();
+cudaError_t forward_impl(const LinearProblem& p, cudaStream_t st) {
+  if (!use_tc()) {
+    ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
+                     OutLayout(p), p.act};
+    simt_gemm<T>(p.x, p.K, 1, p.w, p.K, 1, p.M(), p.N, p.K, ep, st);
+    return cudaGetLastError();
+  }
+  const Layout l = layout_of(p, false);
+  char* ws = static_cast<char*>(p.ws);
+  if (p.dtype == kBF16) return launch_linear_tc(p, p.x, p.w, ws + l.gemm, st);
+  launch_split(p.x, ws + l.x, p.M() * p.K, st);
+  launch_split(p.w, ws + l.w, p.N * p.K, st);
+  return launch_linear_tc(p, ws + l.x, ws + l.w, ws + l.gemm, st);
 }
 
 template <typename T>
 cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
+  constexpr bool f32 = sizeof(T) == 4;
   const int64_t M = p.M();
+  const Layout l = layout_of(p, true);
   char* ws = static_cast<char*>(p.ws);
-  const bool alias = dy_is_du(p);
-  T* du = alias ? nullptr : reinterpret_cast<T*>(ws);
-  float* part = reinterpret_cast<float*>(ws + du_bytes(p));
-  const bool products = p.dx || p.dw;
+  float* part = reinterpret_cast<float*>(ws + l.part);
+  const bool tc = use_tc(), products = p.dx || p.dw;
+  const bool alias = tc ? l.dy_is_du : p.act == kActNone && p.H == 0;
   if (p.db || (!alias && products)) {
     const int64_t blocks = du_row_blocks(M, p.N);
-    launch_du<T>(p, products ? du : nullptr, p.db ? part : nullptr, blocks, st);
-    if (p.db)
-      linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
+    void* du = products && !alias ? ws + l.du : nullptr;
+    if (tc && f32) launch_du<T, true>(p, du, p.db ? part : nullptr, blocks, st);
+    else launch_du<T, false>(p, du, p.db ? part : nullptr, blocks, st);
+    if (p.db) linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
   }
-  const void* g = alias ? p.dy : du;
-  if (use_tc(p)) {
-    void* gws = ws + du_bytes(p) + up256(sizeof(float) * du_row_blocks(M, p.N) * p.N);
-    cudaError_t e;
-    if (p.dx && (e = launch_linear_dx_tc(p, g, gws, st))) return e;
-    if (p.dw && (e = launch_linear_dw_tc(p, g, gws, st))) return e;
+  const void* g = alias ? p.dy : ws + l.du;
+  if (!tc) {
+    if (p.dx) simt_gemm<T>(g, p.N, 1, p.w, 1, p.K, M, p.K, p.N, PlainOut<T>{static_cast<T*>(p.dx), p.K}, st);
+    if (p.dw) simt_gemm<T>(g, 1, p.N, p.x, 1, p.K, p.N, p.K, M, PlainOut<T>{static_cast<T*>(p.dw), p.K}, st);
     return cudaGetLastError();
   }
-  if (p.dx)
-    simt_gemm<T>(g, p.N, 1, p.w, 1, p.K, M, p.K, p.N, PlainOut<T>{static_cast<T*>(p.dx), p.K}, st);
-  if (p.dw)
-    simt_gemm<T>(g, 1, p.N, p.x, 1, p.K, p.N, p.K, M, PlainOut<T>{static_cast<T*>(p.dw), p.K}, st);
+  const void *x = p.x, *w = p.w;
+  if (f32 && p.dx) launch_split(p.w, ws + l.w, p.N * p.K, st), w = ws + l.w;
+  if (f32 && p.dw) launch_split(p.x, ws + l.x, M * p.K, st), x = ws + l.x;
+  cudaError_t e;
+  if (p.dx && (e = launch_linear_dx_tc(p, g, w, ws + l.gemm, st))) return e;
+  if (p.dw && (e = launch_linear_dw_tc(p, g, x, ws + l.gemm, st))) return e;
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(const LinearProblem& p, bool backward) {
-  const bool tc = p.dtype == kBF16;
-  if (!backward) return tc ? gemm_tc_workspace(p.M(), p.N, p.K) : 0;
-  const size_t parts = up256(sizeof(float) * du_row_blocks(p.M(), p.N) * p.N);
-  if (!tc) return du_bytes(p) + parts;
-  const size_t dx = gemm_tc_workspace(p.M(), p.K, p.N), dw = gemm_tc_workspace(p.N, p.K, p.M());
-  return du_bytes(p) + parts + (dx > dw ? dx : dw);
-}
+size_t linear_workspace_bytes(const LinearProblem& p, bool backward) { return layout_of(p, backward).bytes; }
 
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st) {
-  if (use_tc(p)) return launch_linear_tc(p, st);
-  return p.dtype == kBF16 ? forward_simt<__nv_bfloat16>(p, st) : forward_simt<float>(p, st);
+  return p.dtype == kBF16 ? forward_impl<__nv_bfloat16>(p, st) : forward_impl<float>(p, st);
 }
 
 cudaError_t launch_linear_bwd(const LinearProblem& p, cudaStream_t st) {

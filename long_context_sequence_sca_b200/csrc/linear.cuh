@@ -49,6 +49,27 @@ __device__ __forceinline__ void store_f8(__nv_bfloat16* p, const float (&v)[8]) 
                                             pack_bf16x2(v[6], v[7]));
 }
 
+// v = h + m + l in bf16: each plane is the rest of the ones before it rounded to
+// nearest, so what is left is below 2^-25 |v|.  h is cut instead where rounding
+// would carry a finite v to infinity; an infinite v has no rest.
+__device__ __forceinline__ void split3(float v, float& h, float& m, float& l) {
+  h = __bfloat162float(__float2bfloat16_rn(v));
+  if (isinf(h)) h = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+  const float r = isinf(v) ? 0.f : v - h;
+  m = __bfloat162float(__float2bfloat16_rn(r));
+  l = r - m;   // rounded when it is stored
+}
+
+// The planes of 8 values, `plane` elements apart.
+__device__ __forceinline__ void store_planes(__nv_bfloat16* p, int64_t plane, const float (&v)[8]) {
+  float h[8], m[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split3(v[i], h[i], m[i], l[i]);
+  store_f8(p, h);
+  store_f8(p + plane, m);
+  store_f8(p + 2 * plane, l);
+}
+
 // 8 elements as loaded.
 template <typename T> struct Vec8;
 template <> struct Vec8<float> {

@@ -1,7 +1,17 @@
-// The projection's bf16 products on the 5th-generation tensor cores:
+// The projection's products on the 5th-generation tensor cores:
 //   C[m, n] = sum_k A(m, k) B(n, k)
 // with each operand stored along k (K-major) or along its own rows (MN-major),
 // which covers x w^T, du w and du^T x without a transposed copy.
+//
+// fp32 operands come as three bf16 planes, v = h + m + l to 2^-25 of |v|, and
+// the product as the six plane products that reach 2^-24 (the other three are
+// below 2^-26): hh, hm, mh, mm, hl, lh.  To the kernel they are a product six
+// times as deep whose k-blocks come from different planes; at a sixth of the
+// bf16 rate this is still several times the rate of the fp32 FMA pipe.  The
+// tensor core cuts its sums instead of rounding them, by 2^-25.5 of the sum a
+// step on average (measured: 5e-6 after 256 steps), so the planes are added in
+// ascending size, hh last, and a deep product is cut into runs of 2048 whose
+// sums are added with rounding by a second kernel (3e-6 at any depth).
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
 // ring of stages, one thread issues tcgen05.mma, eight warps empty the
@@ -65,18 +75,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 }
 
 template <int CG>
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   if (CG == 1)
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(bar), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
   else   // the barrier may lie in the other CTA of the pair
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
-        "[%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(bar), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -136,9 +146,15 @@ constexpr int kGroupM = 8;           // tiles of one column band done together (
 
 struct GemmShape {
   int64_t M, N;
-  int tiles_m, tiles_n, k_blocks;
+  int tiles_m, tiles_n;
+  int k_blocks, pairs;            // of one plane product; plane products
   int splits, blocks_per_split;   // the k-blocks in `splits` runs, each its own unit
 };
+
+// Planes of A and B of each plane product (one pair, 0 and 0, for bf16).
+constexpr int kPairs = 6;
+__device__ __forceinline__ int plane_a(int left) { return (0x201100 >> (4 * left)) & 15; }
+__device__ __forceinline__ int plane_b(int left) { return (0x021010 >> (4 * left)) & 15; }
 
 struct Unit {
   int m, n, split, kb0, kb1;
@@ -167,17 +183,18 @@ __device__ __forceinline__ Unit unit_at(const GemmShape& g, int u) {
 
 struct None {};
 
+template <typename T>
 struct EpiForward {
   const float* bias;
-  const __nv_bfloat16* residual;
-  __nv_bfloat16 *y, *pre;
+  const T* residual;
+  T *y, *pre;
   OutLayout lay;
   int act;
   struct Band {
     int64_t col;
     float bias[8];
   };
-  using Fetched = uint4;
+  using Fetched = Vec8<T>;
   __device__ __forceinline__ int64_t row(int64_t m) const { return lay.row(m); }
   __device__ __forceinline__ Band band(int n) const {
     Band c;
@@ -188,7 +205,9 @@ struct EpiForward {
     return c;
   }
   __device__ __forceinline__ Fetched fetch(int64_t row, const Band& c, bool on) const {
-    return residual && on ? *reinterpret_cast<const uint4*>(residual + row + c.col) : make_uint4(0, 0, 0, 0);
+    Fetched f;
+    if (residual && on) f.load(residual + row + c.col);
+    return f;
   }
   __device__ __forceinline__ void put(int64_t row, const Band& c, int, const Fetched& f, float (&v)[8]) const {
 #pragma unroll
@@ -203,19 +222,18 @@ struct EpiForward {
       for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kActGelu);
     }
     if (residual) {
-      const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+      float r[8];
+      f.get(r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] += __uint_as_float(w[i] << 16);
-        v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
-      }
+      for (int i = 0; i < 8; ++i) v[i] += r[i];
     }
     store_f8(y + at, v);
   }
 };
 
+template <typename T>
 struct EpiPlain {
-  __nv_bfloat16* c;
+  T* c;
   int N;
   using Band = int;
   using Fetched = None;
@@ -309,23 +327,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
       for (int u = first; u < units && ok; u += step) {
         const Unit t = unit_at(g, u);
         const int m0 = (t.m * CG + (int)rank) * 128, n0 = t.n * kBN + (int)rank * (kBN / CG);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const int s = it % NS;
-          if (it >= NS && !(ok = mbar_wait_cluster(empty + s, (it / NS - 1) & 1, abort_flag, status))) break;
-          if (rank == 0) mbar_arrive_expect_tx(full + s, CG * Cfg::kStage);
-          const uint32_t bar = CG == 1 ? smem_u32(full + s) : map_to(full + s, 0);
-          uint8_t *pa = smem + s * Cfg::kStage, *pb = pa + Cfg::kA;
-          if (AMN) {
+        for (int left = g.pairs - 1; left >= 0 && ok; --left) {
+          const int za = plane_a(left), zb = plane_b(left);
+          for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+            const int s = it % NS;
+            if (it >= NS && !(ok = mbar_wait_cluster(empty + s, (it / NS - 1) & 1, abort_flag, status))) break;
+            if (rank == 0) mbar_arrive_expect_tx(full + s, CG * Cfg::kStage);
+            const uint32_t bar = CG == 1 ? smem_u32(full + s) : map_to(full + s, 0);
+            uint8_t *pa = smem + s * Cfg::kStage, *pb = pa + Cfg::kA;
+            if (AMN) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tma_load<CG>(pa + i * 8192, &ma, bar, m0 + 64 * i, kb * kBK);
-          } else {
-            tma_load<CG>(pa, &ma, bar, kb * kBK, m0);
-          }
-          if (BMN) {
+              for (int i = 0; i < 2; ++i) tma_load<CG>(pa + i * 8192, &ma, bar, m0 + 64 * i, kb * kBK, za);
+            } else {
+              tma_load<CG>(pa, &ma, bar, kb * kBK, m0, za);
+            }
+            if (BMN) {
 #pragma unroll
-            for (int i = 0; i < kBN / CG / 64; ++i) tma_load<CG>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK);
-          } else {
-            tma_load<CG>(pb, &mb, bar, kb * kBK, n0);
+              for (int i = 0; i < kBN / CG / 64; ++i)
+                tma_load<CG>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK, zb);
+            } else {
+              tma_load<CG>(pb, &mb, bar, kb * kBK, n0, zb);
+            }
           }
         }
       }
@@ -352,7 +374,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
         const int acc = k & 1;
         if (k >= 2 && !(ok = mbar_wait_cluster(acc_empty + acc, (k / 2 - 1) & 1, abort_flag, status))) break;
         tc_fence_after();
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int blocks = (t.kb1 - t.kb0) * g.pairs;
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
           const int s = it % NS;
           if (!(ok = mbar_wait_cluster(full + s, (it / NS) & 1, abort_flag, status))) break;
           tc_fence_after();
@@ -362,7 +385,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             umma<CG>(tmem + acc * kBN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
-                     idesc, kb > t.kb0 || kk > 0 ? 1u : 0u);
+                     idesc, kb > 0 || kk > 0 ? 1u : 0u);
           umma_done<CG>(empty + s);
         }
         if (ok) umma_done<CG>(acc_full + acc);
@@ -485,32 +508,27 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [rows, inner] bf16 row-major, boxes of 64 x box_rows with 128-byte swizzle;
-// what lies outside reads as zero.
-cudaError_t make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t inner, int box_rows) {
+// `planes` of [rows, inner] bf16 row-major, boxes of 64 x box_rows with 128-byte
+// swizzle; what lies outside a plane reads as zero.
+cudaError_t make_map(CUtensorMap* m, const void* base, int planes, int64_t rows, int64_t inner, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+  cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)(rows * inner) * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-
-struct Operand {
-  const void* p;
-  bool mn;   // stored [k, rows] instead of [rows, k]
-};
 
 struct GemmPlan {
   int cg;
   GemmShape g;
 };
 
-GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K) {
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes) {
   GemmPlan pl;
   auto tiles = [](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
   pl.cg = M <= 128 ? 1 : 2;
@@ -519,24 +537,31 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K) {
   pl.g.tiles_m = tiles(M, 128 * pl.cg);
   pl.g.tiles_n = tiles(N, kBN);
   pl.g.k_blocks = tiles(K, kBK);
+  pl.g.pairs = planes == 3 ? kPairs : 1;
+  // Few tiles: as many runs as fill the GPU, each of eight k-blocks' work at
+  // least (below 32 the second kernel costs more than the runs save).
   const int64_t slots = sm_count() / pl.cg, t = (int64_t)pl.g.tiles_m * pl.g.tiles_n;
-  int64_t splits = pl.g.k_blocks < 32 ? 1 : slots / t;
-  if (splits > pl.g.k_blocks / 8) splits = pl.g.k_blocks / 8;
-  if (splits < 1) splits = 1;
+  const int64_t work = (int64_t)pl.g.k_blocks * pl.g.pairs;
+  int64_t splits = work < 32 ? 1 : slots / t;
+  if (splits > work / 8) splits = work / 8;
+  if (splits > pl.g.k_blocks) splits = pl.g.k_blocks;
+  // fp32: runs of at most 2048
+  const int64_t least = planes == 3 ? (pl.g.k_blocks + 31) / 32 : 1;
+  if (splits < least) splits = least;
   pl.g.blocks_per_split = (int)((pl.g.k_blocks + splits - 1) / splits);
   pl.g.splits = (pl.g.k_blocks + pl.g.blocks_per_split - 1) / pl.g.blocks_per_split;
   return pl;
 }
 
 template <int CG, bool AMN, bool BMN, class Epi>
-cudaError_t run_gemm(const GemmPlan& pl, const Operand& A, const Operand& B, int64_t K, const Epi& ep, int* status,
-                     cudaStream_t st) {
+cudaError_t run_gemm(const GemmPlan& pl, const void* A, const void* B, int64_t K, int planes, const Epi& ep,
+                     int* status, cudaStream_t st) {
   using Cfg = GemmCfg<CG>;
   CUtensorMap ma, mb;
   cudaError_t e;
   const GemmShape& g = pl.g;
-  if ((e = AMN ? make_map(&ma, A.p, K, g.M, kBK) : make_map(&ma, A.p, g.M, K, 128))) return e;
-  if ((e = BMN ? make_map(&mb, B.p, K, g.N, kBK) : make_map(&mb, B.p, g.N, K, kBN / CG))) return e;
+  if ((e = AMN ? make_map(&ma, A, planes, K, g.M, kBK) : make_map(&ma, A, planes, g.M, K, 128))) return e;
+  if ((e = BMN ? make_map(&mb, B, planes, K, g.N, kBK) : make_map(&mb, B, planes, g.N, K, kBN / CG))) return e;
   auto kern = gemm_tc_kernel<CG, AMN, BMN, Epi>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kAlloc))) return e;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
@@ -556,48 +581,55 @@ cudaError_t run_gemm(const GemmPlan& pl, const Operand& A, const Operand& B, int
 }
 
 template <bool AMN, bool BMN, class Epi>
-cudaError_t gemm_of(const GemmPlan& pl, const Operand& A, const Operand& B, int64_t K, const Epi& ep, int* status,
-                    cudaStream_t st) {
-  return pl.cg == 2 ? run_gemm<2, AMN, BMN, Epi>(pl, A, B, K, ep, status, st)
-                    : run_gemm<1, AMN, BMN, Epi>(pl, A, B, K, ep, status, st);
+cudaError_t gemm_of(const GemmPlan& pl, const void* A, const void* B, int64_t K, int planes, const Epi& ep,
+                    int* status, cudaStream_t st) {
+  return pl.cg == 2 ? run_gemm<2, AMN, BMN, Epi>(pl, A, B, K, planes, ep, status, st)
+                    : run_gemm<1, AMN, BMN, Epi>(pl, A, B, K, planes, ep, status, st);
 }
 
+// A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.
 template <bool AMN, bool BMN, class Epi>
-cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const Epi& ep, void* ws, int* status,
-                 cudaStream_t st) {
-  const GemmPlan pl = gemm_plan(M, N, K);
-  const Operand a{A, AMN}, b{B, BMN};
-  if (pl.g.splits == 1) return gemm_of<AMN, BMN>(pl, a, b, K, ep, status, st);
+cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, int planes, const Epi& ep, void* ws,
+                 int* status, cudaStream_t st) {
+  const GemmPlan pl = gemm_plan(M, N, K, planes);
+  if (pl.g.splits == 1) return gemm_of<AMN, BMN>(pl, A, B, K, planes, ep, status, st);
   float* part = static_cast<float*>(ws);
-  if (cudaError_t e = gemm_of<AMN, BMN>(pl, a, b, K, EpiPartial{part, M, (int)N}, status, st)) return e;
+  if (cudaError_t e = gemm_of<AMN, BMN>(pl, A, B, K, planes, EpiPartial{part, M, (int)N}, status, st)) return e;
   gemm_sum_kernel<Epi><<<(unsigned)((M * N / 8 + 255) / 256), 256, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t forward_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st) {
+  const EpiForward<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
+                         OutLayout(p), p.act};
+  return gemm<false, false>(p.M(), p.N, p.K, x, w, sizeof(T) == 4 ? 3 : 1, ep, ws, p.status, st);
+}
+
 }  // namespace
 
-size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K) {
-  const GemmPlan pl = gemm_plan(M, N, K);
+size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
+  const GemmPlan pl = gemm_plan(M, N, K, dtype == kBF16 ? 1 : 3);
   return pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
 }
 
-cudaError_t launch_linear_tc(const LinearProblem& p, cudaStream_t st) {
-  const EpiForward ep{p.bias,
-                      static_cast<const __nv_bfloat16*>(p.residual),
-                      static_cast<__nv_bfloat16*>(p.y),
-                      static_cast<__nv_bfloat16*>(p.pre),
-                      OutLayout(p),
-                      p.act};
-  return gemm<false, false>(p.M(), p.N, p.K, p.x, p.w, ep, p.ws, p.status, st);
+cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st) {
+  return p.dtype == kBF16 ? forward_tc<__nv_bfloat16>(p, x, w, ws, st) : forward_tc<float>(p, x, w, ws, st);
 }
 
-cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, void* ws, cudaStream_t st) {
-  return gemm<false, true>(p.M(), p.K, p.N, du, p.w, EpiPlain{static_cast<__nv_bfloat16*>(p.dx), (int)p.K}, ws,
+cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, const void* w, void* ws, cudaStream_t st) {
+  if (p.dtype == kBF16)
+    return gemm<false, true>(p.M(), p.K, p.N, du, w, 1, EpiPlain<__nv_bfloat16>{static_cast<__nv_bfloat16*>(p.dx), (int)p.K},
+                             ws, p.status, st);
+  return gemm<false, true>(p.M(), p.K, p.N, du, w, 3, EpiPlain<float>{static_cast<float*>(p.dx), (int)p.K}, ws,
                            p.status, st);
 }
 
-cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, void* ws, cudaStream_t st) {
-  return gemm<true, true>(p.N, p.K, p.M(), du, p.x, EpiPlain{static_cast<__nv_bfloat16*>(p.dw), (int)p.K}, ws,
+cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, const void* x, void* ws, cudaStream_t st) {
+  if (p.dtype == kBF16)
+    return gemm<true, true>(p.N, p.K, p.M(), du, x, 1, EpiPlain<__nv_bfloat16>{static_cast<__nv_bfloat16*>(p.dw), (int)p.K},
+                            ws, p.status, st);
+  return gemm<true, true>(p.N, p.K, p.M(), du, x, 3, EpiPlain<float>{static_cast<float*>(p.dw), (int)p.K}, ws,
                           p.status, st);
 }
 
