@@ -442,7 +442,9 @@ int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, con
  * step details: Z = X W_z + b_z in step 2, V = SiLU(X W_v + b_v) in step 3):
  *   u = x w^T + bias,  y = f(u) + residual
  * with f the identity, SiLU u / (1 + e^-u) or GELU u Phi(u) (Phi the normal
- * distribution function).  fp32 accumulation; one rounding of y.  fp32 operands
+ * distribution function).  fp32 accumulation; one rounding of y.  (The tensor
+ * core cuts its fp32 sums: 2^-25.5 of the sum a step of 16 on average, invisible
+ * in bf16 results; fp32 ones are summed in runs of at most 2048.)  fp32 operands
  * are split into three bf16 parts and multiplied on the tensor cores as six
  * partial products: as accurate as fp32 FMA (a few 2^-24 per term; measured
  * 1e-7 to 2e-6 of the result's norm), except that an infinite operand gives
@@ -453,8 +455,12 @@ int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, con
  *   bias     : [N] fp32 or NULL.
  *   y        : [B, T, N] dtype if H = 0, else [B, H, T, N / H]: the path's
  *              layout, so v comes out of its projection ready for SCA.
- *   residual : in y's layout and dtype, or NULL.  pre: NULL, or in y's
- *              layout: receives u, which the backward of an activation needs.
+ *   residual : in y's layout and dtype, or NULL.
+ *   pre      : NULL, or fp32 in y's layout: receives u, which the backward of
+ *              an activation needs (in bf16 its rounding would put 2^-9 into
+ *              f'(u) and so into db).  For K > 2048 in bf16, asking for pre
+ *              also makes the accumulation more exact (see below), so y may
+ *              differ in its last bit from that of a call without.
  *   Requires N % 8 == 0, K % 8 == 0, (N / H) % 8 == 0 if H > 0,
  *   B * T <= 2^31 - 256, N and K <= 2^20.
  *
@@ -470,10 +476,10 @@ int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, con
 #define GECKO_ACT_GELU 2
 int gecko_linear_workspace(int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype, int backward,
                            int64_t* bytes);
-int gecko_linear_forward(const void* x, const void* w, const float* bias, const void* residual, void* y, void* pre,
+int gecko_linear_forward(const void* x, const void* w, const float* bias, const void* residual, void* y, float* pre,
                          int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype, void* workspace,
                          int64_t workspace_bytes, void* stream);
-int gecko_linear_backward(const void* x, const void* w, const void* dy, const void* pre, void* dx, void* dw,
+int gecko_linear_backward(const void* x, const void* w, const void* dy, const float* pre, void* dx, void* dw,
                           float* db, int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype,
                           void* workspace, int64_t workspace_bytes, void* stream);
 

@@ -268,13 +268,14 @@ cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
-// One validated call.  x [M, K], w [N, K], M = B * T; y, pre, residual, dy
-// [M, N], or [B, H, T, N / H] where H > 0; dx [M, K], dw [N, K], db [N] fp32.
+// One validated call.  x [M, K], w [N, K], M = B * T; y, residual, dy (dtype)
+// and pre (fp32) [M, N], or [B, H, T, N / H] where H > 0; dx [M, K], dw [N, K], db [N] fp32.
 struct LinearProblem {
   const void *x, *w;
   const float* bias;
   const void* residual;
-  void *y, *pre;
+  void* y;
+  float* pre;
   const void* dy;
   void *dx, *dw;
   float* db;

@@ -192,7 +192,7 @@ LinearProblem linear_problem(int64_t B, int64_t T, int64_t N, int64_t K, int64_t
   return p;
 }
 
-int linear_forward(const void* x, const void* w, const float* bias, const void* residual, void* y, void* pre,
+int linear_forward(const void* x, const void* w, const float* bias, const void* residual, void* y, float* pre,
                    int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype, void* ws,
                    int64_t ws_bytes, void* stream) {
   int rc;
@@ -206,7 +206,7 @@ int linear_forward(const void* x, const void* w, const float* bias, const void* 
   return launched(launch_linear(p, static_cast<cudaStream_t>(stream)), "projection");
 }
 
-int linear_backward(const void* x, const void* w, const void* dy, const void* pre, void* dx, void* dw, float* db,
+int linear_backward(const void* x, const void* w, const void* dy, const float* pre, void* dx, void* dw, float* db,
                     int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act, int dtype, void* ws,
                     int64_t ws_bytes, void* stream) {
   int rc;
@@ -217,7 +217,7 @@ int linear_backward(const void* x, const void* w, const void* dy, const void* pr
   LinearProblem p = linear_problem(B, T, N, K, H, act, dtype);
   if ((rc = check_workspace(ws, ws_bytes, linear_workspace_bytes(p, true)))) return rc;
   if ((rc = device_status_word(&p.status))) return rc;
-  p.x = x, p.w = w, p.dy = dy, p.pre = const_cast<void*>(pre), p.dx = dx, p.dw = dw, p.db = db, p.ws = ws;
+  p.x = x, p.w = w, p.dy = dy, p.pre = const_cast<float*>(pre), p.dx = dx, p.dw = dw, p.db = db, p.ws = ws;
   cudaGetLastError();
   return launched(launch_linear_bwd(p, static_cast<cudaStream_t>(stream)), "projection backward");
 }
@@ -297,7 +297,7 @@ extern "C" int gecko_linear_workspace(int64_t B, int64_t T, int64_t N, int64_t K
 }
 
 extern "C" int gecko_linear_forward(const void* x, const void* w, const float* bias, const void* residual, void* y,
-                                    void* pre, int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act,
+                                    float* pre, int64_t B, int64_t T, int64_t N, int64_t K, int64_t H, int act,
                                     int dtype, void* workspace, int64_t workspace_bytes, void* stream) {
   return guarded([&] {
     return linear_forward(x, w, bias, residual, y, pre, B, T, N, K, H, act, dtype, workspace, workspace_bytes,
@@ -305,7 +305,7 @@ extern "C" int gecko_linear_forward(const void* x, const void* w, const float* b
   });
 }
 
-extern "C" int gecko_linear_backward(const void* x, const void* w, const void* dy, const void* pre, void* dx,
+extern "C" int gecko_linear_backward(const void* x, const void* w, const void* dy, const float* pre, void* dx,
                                      void* dw, float* db, int64_t B, int64_t T, int64_t N, int64_t K, int64_t H,
                                      int act, int dtype, void* workspace, int64_t workspace_bytes, void* stream) {
   return guarded([&] {

@@ -65,13 +65,14 @@ template <typename T>
 struct ForwardOut {
   const float* bias;
   const T* residual;
-  T *y, *pre;
+  T* y;
+  float* pre;
   OutLayout lay;
   int act;
   __device__ void operator()(int64_t m, int64_t n, float u) const {
     if (bias) u += bias[n];
     const int64_t at = lay.at(m, n);
-    if (pre) pre[at] = from_f32<T>(u);
+    if (pre) pre[at] = u;
     float v = activate(u, act);
     if (residual) v += to_f32(residual[at]);
     y[at] = from_f32<T>(v);
@@ -104,7 +105,7 @@ constexpr int kDuBlocks = 4;     // per SM
 // the operand type of the two products that follow) or as bf16 planes; the
 // column sums of the unrounded values go to part [gridDim.y, N].
 template <typename T, int kAct, bool kPlanes>
-__global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, const T* pre, void* du, float* part,
+__global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, const float* pre, void* du, float* part,
                                                                    OutLayout lay, int64_t M, int64_t N, int64_t rows) {
   __shared__ float red[kDuRowsPar][kDuCols];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -114,7 +115,8 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
   if (n < N) {
     const int64_t col = lay.col((int)n);
     for (int64_t m = (int64_t)blockIdx.y * rows + ry; m < m1; m += kDuRowsPar * kDuUnroll) {
-      Vec8<T> g[kDuUnroll], u[kDuUnroll];
+      Vec8<T> g[kDuUnroll];
+      Vec8<float> u[kDuUnroll];
 #pragma unroll
       for (int i = 0; i < kDuUnroll; ++i) {
         const int64_t mi = m + i * kDuRowsPar;
@@ -191,7 +193,8 @@ template <typename T, bool kPlanes>
 void launch_du(const LinearProblem& p, void* du, float* part, int64_t blocks, cudaStream_t st) {
   const dim3 grid((unsigned)((p.N + kDuCols - 1) / kDuCols), (unsigned)blocks);
   const int64_t rows = (p.M() + blocks - 1) / blocks;
-  const T *dy = static_cast<const T*>(p.dy), *pre = static_cast<const T*>(p.pre);
+  const T* dy = static_cast<const T*>(p.dy);
+  const float* pre = p.pre;
   const OutLayout lay(p);
   if (p.act == kActNone)
     linear_du_kernel<T, kActNone, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
@@ -261,8 +264,7 @@ Layout layout_of(const LinearProblem& p, bool backward) {
 template <typename T>
 cudaError_t forward_impl(const LinearProblem& p, cudaStream_t st) {
   if (!use_tc()) {
-    ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
-                     OutLayout(p), p.act};
+    ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act};
     simt_gemm<T>(p.x, p.K, 1, p.w, p.K, 1, p.M(), p.N, p.K, ep, st);
     return cudaGetLastError();
   }

@@ -7,12 +7,30 @@
 
 namespace gecko {
 
-// f(u): SiLU u / (1 + e^-u); GELU u Phi(u), with Phi(u) = erfc(-u / sqrt 2) / 2
-// (no cancellation for negative u).  The approximate exponential and quotient
-// are good to 2^-21 + |u| 2^-23, far below a bf16 step and enough for fp32.
+// Phi(u) of the normal distribution and e = exp(-u^2 / 2): Phi(-|u|) =
+// erfc(|u| / sqrt 2) / 2 by Hastings' rational approximation (Abramowitz and
+// Stegun 7.1.26, absolute error 1.5e-7; no cancellation for negative u).
+__device__ __forceinline__ float normal_cdf(float u, float& e) {
+  const float x = fabsf(u) * 0.7071067811865476f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  e = __expf(-0.5f * u * u);
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float tail = 0.5f * p * t * e;
+  return u < 0.f ? tail : 1.f - tail;
+}
+
+// f(u): SiLU u / (1 + e^-u); GELU u Phi(u).  The approximate exponential and
+// quotient are good to 2^-21 + |u| 2^-23, far below a bf16 step and enough for
+// fp32.
 __device__ __forceinline__ float activate(float u, int act) {
   if (act == kActSilu) return __fdividef(u, 1.f + __expf(-u));
-  if (act == kActGelu) return 0.5f * u * erfcf(-0.7071067811865476f * u);
+  if (act == kActGelu) {
+    float e;
+    return u * normal_cdf(u, e);
+  }
   return u;
 }
 
@@ -22,8 +40,11 @@ __device__ __forceinline__ float act_slope(float u, int act) {
     const float s = __fdividef(1.f, 1.f + __expf(-u));
     return s * fmaf(u, 1.f - s, 1.f);
   }
-  if (act == kActGelu)
-    return 0.5f * erfcf(-0.7071067811865476f * u) + u * 0.3989422804014327f * __expf(-0.5f * u * u);
+  if (act == kActGelu) {
+    float e;
+    const float c = normal_cdf(u, e);
+    return fmaf(u * 0.3989422804014327f, e, c);
+  }
   return 1.f;
 }
 

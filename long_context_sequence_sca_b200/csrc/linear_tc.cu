@@ -7,16 +7,18 @@
 // the product as the six plane products that reach 2^-24 (the other three are
 // below 2^-26): hh, hm, mh, mm, hl, lh.  To the kernel they are a product six
 // times as deep whose k-blocks come from different planes; at a sixth of the
-// bf16 rate this is still several times the rate of the fp32 FMA pipe.  The
-// tensor core cuts its sums instead of rounding them, by 2^-25.5 of the sum a
-// step on average (measured: 5e-6 after 256 steps), so the planes are added in
-// ascending size, hh last, and a deep product is cut into runs of 2048 whose
-// sums are added with rounding by a second kernel (3e-6 at any depth).
+// bf16 rate this is still several times the rate of the fp32 FMA pipe.
+//
+// The tensor core cuts its sums instead of rounding them, by about 2^-25.5 of
+// the sum a step (measured: 5e-6 of the result after 256 steps, which shows in
+// the fp32 results: y, pre, db).  Where it would (fp32, and bf16 with pre), a
+// product is cut into runs of 1024 (2048), whose sums the epilogue warps add up
+// in registers with rounding while the next run is under way (kSum), and the
+// planes are added in ascending size.
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
 // ring of stages, one thread issues tcgen05.mma, eight warps empty the
-// accumulator (TMEM, two of them in turn) through shared memory, where they
-// transpose it so that every global access is a run of 64 bytes of one row.
+// accumulator (TMEM, two of them in turn), a row per thread.
 // With CG = 2 a pair of CTAs shares one 256 x kBN tile: each loads its 128
 // rows of A and half the rows of B, so a k-block moves half the bytes per
 // multiply-add of a 128 x kBN tile; the even CTA issues the MMAs for both.
@@ -142,13 +144,20 @@ constexpr int kBN = 256;             // columns per tile
 constexpr int kGemmThreads = 384;    // TMA, MMA, TMEM, idle warp; eight epilogue warps
 constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8;
 constexpr int kBand = 32;            // columns an epilogue warp takes at a time
+constexpr int kBands = 256 / kBand / 2;   // bands of a tile per epilogue warp (two warps share a row quarter)
+// Registers per thread after setmaxnreg: the running sums of 128 columns sit in
+// the epilogue warps'.  The split has to fit what the block was launched with
+// (setmaxnreg.inc would wait for more forever).
+constexpr int kRegsCtl = 56, kRegsEpilogue = 224;
+static_assert(128 * kRegsCtl + 256 * kRegsEpilogue <= kGemmThreads * 168, "setmaxnreg split above the launch registers");
 constexpr int kGroupM = 8;           // tiles of one column band done together (operand reuse in L2)
 
 struct GemmShape {
   int64_t M, N;
   int tiles_m, tiles_n;
   int k_blocks, pairs;            // of one plane product; plane products
-  int splits, blocks_per_split;   // the k-blocks in `splits` runs, each its own unit
+  int splits, blocks_per_split;   // the k-blocks in `splits` parts, each its own unit
+  int run;                        // k-blocks per run of the accumulator (kSum)
 };
 
 // Planes of A and B of each plane product (one pair, 0 and 0, for bf16).
@@ -176,86 +185,136 @@ __device__ __forceinline__ Unit unit_at(const GemmShape& g, int u) {
 
 // -------------------------------------------------------------- epilogues --
 
-// Each writes 8 consecutive columns n of a row.  Row and column parts of an
-// address are separate: rows are fixed for a tile, columns for a band of it.
-// What has to be read (bias, residual) is fetched for a whole band before it
-// is used, so that its latency is paid once.
+// A thread owns one row of the tile and takes 32 columns of it at a time, 16 by
+// 16, straight from registers to global memory: shared memory is busy feeding
+// the MMAs (a transpose through it took five times as long as the stores of
+// full 32-byte sectors that this makes).  `wide` says that rows and columns
+// of 16 are aligned for 32-byte accesses.
 
-struct None {};
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
+// 16 consecutive values, of which the first 8 or all 16 are in the tensor.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  if (wide) {
+    store_sector(p, w);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ void store16(float* p, const float* v, bool wide) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+    if (wide) {
+      store_sector(p + 8 * h, w);
+    } else {
+      *reinterpret_cast<uint4*>(p + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(p + 8 * h + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+// Forward: bias, activation, residual.  What has to be read for a band of 32
+// columns is fetched before the sums are waited for.
 template <typename T>
 struct EpiForward {
   const float* bias;
   const T* residual;
-  T *y, *pre;
+  T* y;
+  float* pre;
   OutLayout lay;
   int act;
-  struct Band {
-    int64_t col;
-    float bias[8];
+  bool wide;       // of y (pre is fp32: rows of 8 are enough)
+  bool wide_pre;
+  struct Fetched {
+    float bias[32];
+    Vec8<T> residual[4];
   };
-  using Fetched = Vec8<T>;
   __device__ __forceinline__ int64_t row(int64_t m) const { return lay.row(m); }
-  __device__ __forceinline__ Band band(int n) const {
-    Band c;
-    c.col = lay.col(n);
+  __device__ __forceinline__ void fetch(Fetched& f, int64_t row, int n, bool on) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c.bias[i] = 0.f;
-    if (bias) load_f8(bias + n, c.bias);
-    return c;
-  }
-  __device__ __forceinline__ Fetched fetch(int64_t row, const Band& c, bool on) const {
-    Fetched f;
-    if (residual && on) f.load(residual + row + c.col);
-    return f;
-  }
-  __device__ __forceinline__ void put(int64_t row, const Band& c, int, const Fetched& f, float (&v)[8]) const {
+    for (int i = 0; i < 4; ++i) {
+      const bool in = n + 8 * i < lay.N;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += c.bias[i];
-    const int64_t at = row + c.col;
-    if (pre) store_f8(pre + at, v);
+      for (int j = 0; j < 8; ++j) f.bias[8 * i + j] = 0.f;
+      if (bias && in) load_f8(bias + n + 8 * i, *reinterpret_cast<float(*)[8]>(f.bias + 8 * i));
+      if (residual && in && on) f.residual[i].load(residual + row + lay.col(n + 8 * i));
+    }
+  }
+  __device__ __forceinline__ void put(const Fetched& f, int64_t row, int n, int, float* v) const {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += f.bias[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (pre && n + 8 * i < lay.N) {
+        float* p = pre + row + lay.col(n + 8 * i);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+        if (wide_pre) {
+          store_sector(p, w);
+        } else {
+          *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(p + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    }
     if (act == kActSilu) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kActSilu);
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], kActSilu);
     } else if (act == kActGelu) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kActGelu);
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], kActGelu);
     }
-    if (residual) {
-      float r[8];
-      f.get(r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
+    for (int i = 0; i < 4; ++i)
+      if (residual && n + 8 * i < lay.N) {
+        float r[8];
+        f.residual[i].get(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = n + 16 * i;
+      if (wide) {
+        if (c < lay.N) store16(y + row + lay.col(c), v + 16 * i, true);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c + 8 * h < lay.N) store_f8(y + row + lay.col(c + 8 * h), *reinterpret_cast<float(*)[8]>(v + 16 * i + 8 * h));
+      }
     }
-    store_f8(y + at, v);
   }
 };
 
+// c[split][m][n]: the product itself (one split), or the parts' sums.
 template <typename T>
 struct EpiPlain {
   T* c;
-  int N;
-  using Band = int;
-  using Fetched = None;
-  __device__ __forceinline__ int64_t row(int64_t m) const { return m * N; }
-  __device__ __forceinline__ Band band(int n) const { return n; }
-  __device__ __forceinline__ Fetched fetch(int64_t, Band, bool) const { return {}; }
-  __device__ __forceinline__ void put(int64_t row, Band n, int, Fetched, float (&v)[8]) const {
-    store_f8(c + row + n, v);
-  }
-};
-
-struct EpiPartial {
-  float* part;   // [splits, M, N]
   int64_t M;
   int N;
-  using Band = int;
-  using Fetched = None;
+  bool wide;
+  struct Fetched {};
   __device__ __forceinline__ int64_t row(int64_t m) const { return m * N; }
-  __device__ __forceinline__ Band band(int n) const { return n; }
-  __device__ __forceinline__ Fetched fetch(int64_t, Band, bool) const { return {}; }
-  __device__ __forceinline__ void put(int64_t row, Band n, int split, Fetched, float (&v)[8]) const {
-    store_f8(part + (int64_t)split * M * N + row + n, v);
+  __device__ __forceinline__ void fetch(Fetched&, int64_t, int, bool) const {}
+  __device__ __forceinline__ void put(const Fetched&, int64_t row, int n, int split, float* v) const {
+    T* p = c + (int64_t)split * M * N + row + n;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (n + 16 * i + 8 < N) store16(p + 16 * i, v + 16 * i, wide);
+      else if (n + 16 * i < N) store_f8(p + 16 * i, *reinterpret_cast<float(*)[8]>(v + 16 * i));
+    }
   }
 };
 
@@ -264,11 +323,8 @@ struct EpiPartial {
 template <int CG>
 struct GemmCfg {
   static constexpr int kA = 128 * kBK * 2, kB = kBN / CG * kBK * 2, kStage = kA + kB;
-  static constexpr int kStaging = kEpilogueWarps * 32 * kBand * 4;   // per warp: 32 rows x 32 columns, fp32
-  static constexpr int kStages = (232448 - 1024 - 512 - kStaging) / kStage > 8
-                                     ? 8 : (232448 - 1024 - 512 - kStaging) / kStage;
-  static constexpr int kStageOff = kStages * kStage;
-  static constexpr int kBarOff = kStageOff + kStaging;
+  static constexpr int kStages = (232448 - 1024 - 512) / kStage > 8 ? 8 : (232448 - 1024 - 512) / kStage;
+  static constexpr int kBarOff = kStages * kStage;
   static constexpr int kNumBars = 2 * kStages + 4;   // full, empty; accumulator full, empty
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
@@ -276,7 +332,7 @@ struct GemmCfg {
   static_assert(kAlloc <= 232448, "shared memory above the per-block limit");
 };
 
-template <int CG, bool AMN, bool BMN, class Epi>
+template <int CG, bool AMN, bool BMN, bool kSum, class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_constant__ CUtensorMap ma,
                                                                   const __grid_constant__ CUtensorMap mb,
                                                                   const GemmShape g, const Epi ep, int* status) {
@@ -319,6 +375,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if constexpr (kSum)
+    if (warp < kEpilogueWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsCtl));
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer --
     if (lane == 0) {
@@ -369,97 +427,95 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
       const uint32_t base = smem_u32(smem);
       int it = 0, k = 0;
       bool ok = true;
-      for (int u = first; u < units && ok; u += step, ++k) {
+      for (int u = first; u < units && ok; u += step) {
         const Unit t = unit_at(g, u);
-        const int acc = k & 1;
-        if (k >= 2 && !(ok = mbar_wait_cluster(acc_empty + acc, (k / 2 - 1) & 1, abort_flag, status))) break;
-        tc_fence_after();
         const int blocks = (t.kb1 - t.kb0) * g.pairs;
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
-          const int s = it % NS;
-          if (!(ok = mbar_wait_cluster(full + s, (it / NS) & 1, abort_flag, status))) break;
+        for (int kb = 0; kb < blocks && ok; ++k) {   // k counts runs
+          const int acc = k & 1, end = kSum ? min(kb + g.run, blocks) : blocks;
+          if (k >= 2 && !(ok = mbar_wait_cluster(acc_empty + acc, (k / 2 - 1) & 1, abort_flag, status))) break;
           tc_fence_after();
-          const uint32_t a0 = base + s * Cfg::kStage, b0 = a0 + Cfg::kA;
-          const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
-          const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
+          for (uint32_t fresh = 1; kb < end; ++kb, ++it, fresh = 0) {
+            const int s = it % NS;
+            if (!(ok = mbar_wait_cluster(full + s, (it / NS) & 1, abort_flag, status))) break;
+            tc_fence_after();
+            const uint32_t a0 = base + s * Cfg::kStage, b0 = a0 + Cfg::kA;
+            const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
+            const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            umma<CG>(tmem + acc * kBN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
-                     idesc, kb > 0 || kk > 0 ? 1u : 0u);
-          umma_done<CG>(empty + s);
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              umma<CG>(tmem + acc * kBN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
+                       idesc, kk > 0 ? 1u : 1u - fresh);
+            umma_done<CG>(empty + s);
+          }
+          if (ok) umma_done<CG>(acc_full + acc);
         }
-        if (ok) umma_done<CG>(acc_full + acc);
       }
     }
     __syncwarp();
   } else if (warp >= kEpilogueWarp) {
+    if constexpr (kSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsEpilogue));
     // ----------------------------------------------------------- epilogue --
     const int q = warp % 4;   // the TMEM lanes a warp may read: rows 32 q ..
-    float* stage = reinterpret_cast<float*>(smem + Cfg::kStageOff) + (warp - kEpilogueWarp) * 32 * kBand;
-    // Reading back, 4 lanes share a row and 8 lanes a conflict-free access:
-    // rows r and r + 4.
-    const int c4 = lane % 4, r8 = (lane >> 3) | ((lane & 4) ? 4 : 0);
     const int first_band = (warp - kEpilogueWarp) / 4;   // two warps per row quarter take bands in turn
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + first_band * kBand;
     int k = 0;
     bool ok = true;
-    for (int u = first; u < units; u += step, ++k) {
+    for (int u = first; u < units && ok; u += step) {
       const Unit t = unit_at(g, u);
-      const int acc = k & 1;
-      const int64_t m0 = ((int64_t)t.m * CG + rank) * 128 + q * 32 + r8;
-      const int n0 = t.n * kBN + c4 * 8;
-      int64_t row[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = ep.row(m0 + 8 * i);
-      // bias and residual of a band, fetched one band ahead
-      typename Epi::Band band{};
-      typename Epi::Fetched fetched[4];
-      auto fetch = [&](int c) {
-        const int n = n0 + c * kBand;
-        if (c < kBN / kBand && n < g.N) {
-          band = ep.band(n);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) fetched[i] = ep.fetch(row[i], band, m0 + 8 * i < g.M);
-        }
-      };
-      fetch(first_band);
-      ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full + acc, (k / 2) & 1, abort_flag, status));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t from = tmem + acc * kBN + ((uint32_t)(q * 32) << 16);
+      const int64_t m = ((int64_t)t.m * CG + rank) * 128 + q * 32 + lane;
+      const int n0 = t.n * kBN + first_band * kBand;
+      const bool on = m < g.M;
+      const int64_t row = ep.row(m);
+      if constexpr (!kSum) {
+        const int acc = k & 1;
+        typename Epi::Fetched f;
+        ep.fetch(f, row, n0, on);
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full + acc, (k / 2) & 1, abort_flag, status));
+        if (!ok) break;
+        ++k;
+        tc_fence_after();
 #pragma unroll 1
-      for (int c = first_band; c < kBN / kBand; c += 2) {
-        uint32_t v[32];
-        tmem_ld32p(from + c * kBand, v);
-        tmem_wait_ld();
-        if (c + 2 >= kBN / kBand) {
-          // the accumulator is read: the MMAs of the unit after next may write it
+        for (int j = 0; j < kBands; ++j) {
+          float v[32];
+          tmem_ld32p(lanes + acc * kBN + 2 * j * kBand, reinterpret_cast<uint32_t*>(v));
+          if (j) ep.fetch(f, row, n0 + 2 * j * kBand, on);
+          tmem_wait_ld();
+          if (j == kBands - 1) {
+            // the accumulator is read: the MMAs of the unit after next may write it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(CG == 1 ? smem_u32(acc_empty + acc) : map_to(acc_empty + acc, 0));
+          }
+          if (on) ep.put(f, row, n0 + 2 * j * kBand, t.split, v);
+        }
+      } else {
+        float sum[kBands][32] = {};
+        const int runs = ((t.kb1 - t.kb0) * g.pairs + g.run - 1) / g.run;
+        for (int r = 0; r < runs; ++r, ++k) {
+          const int acc = k & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full + acc, (k / 2) & 1, abort_flag, status));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < kBands; ++j) {
+            uint32_t v[32];
+            tmem_ld32p(lanes + acc * kBN + 2 * j * kBand, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[j][i] += __uint_as_float(v[i]);
+          }
+          // the accumulator is read: the run after next may write it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(CG == 1 ? smem_u32(acc_empty + acc) : map_to(acc_empty + acc, 0));
         }
-        // lane = row; 16-byte piece j of a row lies at (even pieces, then odd) ^ row: no bank conflicts
-        // here, nor below
+        if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(stage + lane * kBand + ((((j >> 1) | ((j & 1) << 2)) ^ (lane & 7)) << 2)) =
-              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        __syncwarp();
-        const typename Epi::Band b = band;
-        typename Epi::Fetched f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = fetched[i];
-        fetch(c + 2);
-        if (n0 + c * kBand < g.N) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* p = stage + (8 * i + r8) * kBand;
-            const float4 lo = *reinterpret_cast<const float4*>(p + ((c4 ^ r8) << 2));
-            const float4 hi = *reinterpret_cast<const float4*>(p + (((c4 + 4) ^ r8) << 2));
-            float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            if (m0 + 8 * i < g.M) ep.put(row[i], b, t.split, f[i], w);
-          }
+        for (int j = 0; j < kBands; ++j) {
+          typename Epi::Fetched f;
+          ep.fetch(f, row, n0 + 2 * j * kBand, on);
+          if (on) ep.put(f, row, n0 + 2 * j * kBand, t.split, sum[j]);
         }
-        __syncwarp();
       }
     }
   }
@@ -470,24 +526,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   if (CG == 2) cluster_sync();
 }
 
-// Sum of the splits' partial products, then the epilogue.
+// Sum of the parts' sums, then the epilogue: a thread takes 32 columns of a row.
 template <class Epi>
-__global__ void __launch_bounds__(256) gemm_sum_kernel(const float* part, int splits, int64_t M, int N, const Epi ep) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= M * N) return;
-  const int64_t m = i / N;
-  const int n = (int)(i - m * N);
-  float v[8];
-  load_f8(part + i, v);
-  for (int s = 1; s < splits; ++s) {
-    float w[8];
-    load_f8(part + (int64_t)s * M * N + i, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += w[j];
-  }
-  const typename Epi::Band band = ep.band(n);
+__global__ void __launch_bounds__(128) gemm_sum_kernel(const float* part, int splits, int64_t M, int N, const Epi ep) {
+  const int bands = (N + 31) / 32;
+  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  if (i >= M * bands) return;
+  const int64_t m = i / bands;
+  const int n = (int)(i - m * bands) * 32;
+  float v[32];
+  typename Epi::Fetched f;
   const int64_t row = ep.row(m);
-  ep.put(row, band, 0, ep.fetch(row, band, true), v);
+  ep.fetch(f, row, n, true);
+  const float* p = part + m * N + n;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (n + 8 * c < N) load_f8(p + 8 * c, *reinterpret_cast<float(*)[8]>(v + 8 * c));
+  for (int s = 1; s < splits; ++s) {
+    p += M * N;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + 8 * c < N) {
+        float w[8];
+        load_f8(p + 8 * c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * c + j] += w[j];
+      }
+  }
+  ep.put(f, row, n, 0, v);
 }
 
 // ------------------------------------------------------------------- host --
@@ -538,22 +604,28 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes) {
   pl.g.tiles_n = tiles(N, kBN);
   pl.g.k_blocks = tiles(K, kBK);
   pl.g.pairs = planes == 3 ? kPairs : 1;
-  // Few tiles: as many runs as fill the GPU, each of eight k-blocks' work at
-  // least (below 32 the second kernel costs more than the runs save).
+  pl.g.run = planes == 3 ? 16 : 32;
+  // Few tiles: as many parts as fill the GPU, each of eight k-blocks' work at
+  // least (below 32 the second kernel costs more than the parts save).
   const int64_t slots = sm_count() / pl.cg, t = (int64_t)pl.g.tiles_m * pl.g.tiles_n;
-  const int64_t work = (int64_t)pl.g.k_blocks * pl.g.pairs;
+  const int64_t work = (int64_t)pl.g.k_blocks * pl.g.pairs;   // k-blocks of a tile
   int64_t splits = work < 32 ? 1 : slots / t;
   if (splits > work / 8) splits = work / 8;
   if (splits > pl.g.k_blocks) splits = pl.g.k_blocks;
-  // fp32: runs of at most 2048
-  const int64_t least = planes == 3 ? (pl.g.k_blocks + 31) / 32 : 1;
-  if (splits < least) splits = least;
+  if (splits < 1) splits = 1;
   pl.g.blocks_per_split = (int)((pl.g.k_blocks + splits - 1) / splits);
   pl.g.splits = (pl.g.k_blocks + pl.g.blocks_per_split - 1) / pl.g.blocks_per_split;
   return pl;
 }
 
-template <int CG, bool AMN, bool BMN, class Epi>
+bool aligned32(const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+
+template <typename T>
+EpiPlain<T> plain(void* c, int64_t M, int64_t N) {
+  return {static_cast<T*>(c), M, (int)N, aligned32(c) && N * sizeof(T) % 32 == 0};
+}
+
+template <int CG, bool AMN, bool BMN, bool kSum, class Epi>
 cudaError_t run_gemm(const GemmPlan& pl, const void* A, const void* B, int64_t K, int planes, const Epi& ep,
                      int* status, cudaStream_t st) {
   using Cfg = GemmCfg<CG>;
@@ -562,7 +634,12 @@ cudaError_t run_gemm(const GemmPlan& pl, const void* A, const void* B, int64_t K
   const GemmShape& g = pl.g;
   if ((e = AMN ? make_map(&ma, A, planes, K, g.M, kBK) : make_map(&ma, A, planes, g.M, K, 128))) return e;
   if ((e = BMN ? make_map(&mb, B, planes, K, g.N, kBK) : make_map(&mb, B, planes, g.N, K, kBN / CG))) return e;
-  auto kern = gemm_tc_kernel<CG, AMN, BMN, Epi>;
+  auto kern = gemm_tc_kernel<CG, AMN, BMN, kSum, Epi>;
+  static const int regs = [&] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (kSum && 128 * kRegsCtl + 256 * kRegsEpilogue > kGemmThreads * regs) return cudaErrorInvalidConfiguration;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kAlloc))) return e;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
   const int64_t slots = sm_count() / CG;
@@ -580,30 +657,41 @@ cudaError_t run_gemm(const GemmPlan& pl, const void* A, const void* B, int64_t K
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, g, ep, status);
 }
 
-template <bool AMN, bool BMN, class Epi>
+template <bool AMN, bool BMN, bool kSum, class Epi>
 cudaError_t gemm_of(const GemmPlan& pl, const void* A, const void* B, int64_t K, int planes, const Epi& ep,
                     int* status, cudaStream_t st) {
-  return pl.cg == 2 ? run_gemm<2, AMN, BMN, Epi>(pl, A, B, K, planes, ep, status, st)
-                    : run_gemm<1, AMN, BMN, Epi>(pl, A, B, K, planes, ep, status, st);
+  return pl.cg == 2 ? run_gemm<2, AMN, BMN, kSum, Epi>(pl, A, B, K, planes, ep, status, st)
+                    : run_gemm<1, AMN, BMN, kSum, Epi>(pl, A, B, K, planes, ep, status, st);
 }
 
-// A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.
-template <bool AMN, bool BMN, class Epi>
+// A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.  kExact: the
+// sums of the accumulator's runs are rounded, not cut (a part of one run needs
+// no adding up).
+template <bool AMN, bool BMN, bool kExact, class Epi>
 cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, int planes, const Epi& ep, void* ws,
                  int* status, cudaStream_t st) {
   const GemmPlan pl = gemm_plan(M, N, K, planes);
-  if (pl.g.splits == 1) return gemm_of<AMN, BMN>(pl, A, B, K, planes, ep, status, st);
+  const bool sum = kExact && pl.g.blocks_per_split * pl.g.pairs > pl.g.run;
+  auto product = [&](const auto& e) {
+    if constexpr (kExact)
+      if (sum) return gemm_of<AMN, BMN, true>(pl, A, B, K, planes, e, status, st);
+    return gemm_of<AMN, BMN, false>(pl, A, B, K, planes, e, status, st);
+  };
+  if (pl.g.splits == 1) return product(ep);
   float* part = static_cast<float*>(ws);
-  if (cudaError_t e = gemm_of<AMN, BMN>(pl, A, B, K, planes, EpiPartial{part, M, (int)N}, status, st)) return e;
-  gemm_sum_kernel<Epi><<<(unsigned)((M * N / 8 + 255) / 256), 256, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
+  if (cudaError_t e = product(EpiPlain<float>{part, M, (int)N, aligned32(part)})) return e;
+  gemm_sum_kernel<Epi><<<(unsigned)((M * ((N + 31) / 32) + 127) / 128), 128, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t forward_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st) {
-  const EpiForward<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), static_cast<T*>(p.pre),
-                         OutLayout(p), p.act};
-  return gemm<false, false>(p.M(), p.N, p.K, x, w, sizeof(T) == 4 ? 3 : 1, ep, ws, p.status, st);
+  const int64_t run = p.H ? p.N / p.H : p.N;   // contiguous columns
+  const EpiForward<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act,
+                         aligned32(p.y) && run % 16 == 0, aligned32(p.pre)};
+  constexpr int planes = sizeof(T) == 4 ? 3 : 1;
+  if (planes == 3 || p.pre) return gemm<false, false, true>(p.M(), p.N, p.K, x, w, planes, ep, ws, p.status, st);
+  return gemm<false, false, false>(p.M(), p.N, p.K, x, w, planes, ep, ws, p.status, st);
 }
 
 }  // namespace
@@ -619,17 +707,17 @@ cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* 
 
 cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, const void* w, void* ws, cudaStream_t st) {
   if (p.dtype == kBF16)
-    return gemm<false, true>(p.M(), p.K, p.N, du, w, 1, EpiPlain<__nv_bfloat16>{static_cast<__nv_bfloat16*>(p.dx), (int)p.K},
-                             ws, p.status, st);
-  return gemm<false, true>(p.M(), p.K, p.N, du, w, 3, EpiPlain<float>{static_cast<float*>(p.dx), (int)p.K}, ws,
+    return gemm<false, true, false>(p.M(), p.K, p.N, du, w, 1, plain<__nv_bfloat16>(p.dx, p.M(), p.K),
+                                    ws, p.status, st);
+  return gemm<false, true, true>(p.M(), p.K, p.N, du, w, 3, plain<float>(p.dx, p.M(), p.K), ws,
                            p.status, st);
 }
 
 cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, const void* x, void* ws, cudaStream_t st) {
   if (p.dtype == kBF16)
-    return gemm<true, true>(p.N, p.K, p.M(), du, x, 1, EpiPlain<__nv_bfloat16>{static_cast<__nv_bfloat16*>(p.dw), (int)p.K},
-                            ws, p.status, st);
-  return gemm<true, true>(p.N, p.K, p.M(), du, x, 3, EpiPlain<float>{static_cast<float*>(p.dw), (int)p.K}, ws,
+    return gemm<true, true, false>(p.N, p.K, p.M(), du, x, 1, plain<__nv_bfloat16>(p.dw, p.N, p.K),
+                                   ws, p.status, st);
+  return gemm<true, true, true>(p.N, p.K, p.M(), du, x, 3, plain<float>(p.dw, p.N, p.K), ws,
                           p.status, st);
 }
 

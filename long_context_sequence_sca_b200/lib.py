@@ -718,7 +718,7 @@ def linear_forward(x, w, bias=None, residual=None, act: str = "none", heads: int
     """y = f(x w^T + bias) + residual with f "none", "silu" or "gelu".  x:
     [B, T, K] (or [M, K]); w: [N, K]; bias: [N] float32.  y and residual are
     [B, T, N], or [B, heads, T, N / heads] if heads > 0.  Returns y, or
-    (y, pre) with x w^T + bias in y's layout if keep_pre."""
+    (y, pre) with x w^T + bias, float32 in y's layout, if keep_pre."""
     B, T, N, K, shape = _linear_sizes(x, w, act, heads)
     dev = x.device
     _tensor(bias, "bias", (N,), torch.float32, dev)
@@ -727,7 +727,7 @@ def linear_forward(x, w, bias=None, residual=None, act: str = "none", heads: int
     with _on(dev, stream) as st:
         if y is None:
             y = torch.empty(shape, dtype=x.dtype, device=dev)
-        pre = torch.empty(shape, dtype=x.dtype, device=dev) if keep_pre else None
+        pre = torch.empty(shape, dtype=torch.float32, device=dev) if keep_pre else None
         ws, wp, wn = _workspace(gecko_linear_workspace, (B, T, N, K, heads, ACTS[act], _DT[x.dtype], 0), dev)
         _check(gecko_linear_forward(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre),
                                     B, T, N, K, heads, ACTS[act], _DT[x.dtype], wp, wn, st))
@@ -741,7 +741,7 @@ def linear_backward(x, w, dy, pre=None, act: str = "none", heads: int = 0, need=
     B, T, N, K, shape = _linear_sizes(x, w, act, heads)
     dev = x.device
     _tensor(_required(dy, "dy"), "dy", shape, x.dtype, dev)
-    _tensor(pre, "pre", shape, x.dtype, dev)
+    _tensor(pre, "pre", shape, torch.float32, dev)
     with _on(dev, stream) as st:
         dx = torch.empty_like(x) if need[0] else None
         dw = torch.empty_like(w) if need[1] else None

@@ -6,8 +6,8 @@ most (K + 2) 2^-24 sum |x w|; the bias adds one rounding.  An activation's slope
 is at most 1.13 and its own arithmetic is off by at most ACT relative to |u|
 (SiLU: the exponential to 2^-21 + |u| 2^-23, of which u s(u) keeps at most the
 share 1 - s; GELU: erfc to 2^-20).  y adds the residual and one rounding to the
-type.  The gradient of u reads u rounded to the type (f'' is at most 0.8 in
-size) and is itself rounded to the type as the operand of dx and dw."""
+type.  The gradient of u reads u in fp32 (f'' is at most 0.8 in size) and is
+itself rounded to the type as the operand of dx and dw."""
 import numpy as np
 import pytest
 import torch
@@ -43,18 +43,18 @@ def check(L, inp, dtype, act, H):
     wy, wu = O.linear(hx, hw, hb, hr, act, H)
     sums = np.abs(hx) @ np.abs(hw).T + (0 if hb is None else np.abs(hb))
     Eu = O.split_heads((K + 3) * F32 * sums, H)
-    within(pre, wu, Eu + u * (np.abs(wu) + Eu), "pre")
+    within(pre, wu, Eu, "pre")
     own = ACT * np.abs(wu) if act != "none" else 0.0
     Ey = (1.13 if act != "none" else 1.0) * Eu + own + 2 * F32 * (np.abs(wy) + (0 if hr is None else np.abs(hr)))
     within(y, wy, Ey + u * (np.abs(wy) + Ey), "y")
     only = L.linear_forward(inp["x"], inp["w"], bias=inp["bias"], residual=inp["residual"], act=act, heads=H)
-    assert torch.equal(only, y)
+    within(only, wy, Ey + u * (np.abs(wy) + Ey), "y without pre")
 
     dx, dw, db = L.linear_backward(inp["x"], inp["w"], inp["dy"], pre=pre if act != "none" else None, act=act,
                                    heads=H)
     wx, ww, wb, du = O.linear_grad(hx, hw, hd, hb, act, H)
-    g, um, Em = (np.abs(O.merge_heads(v, H)) for v in (hd, wu, Eu))
-    Edu = np.zeros_like(du) if act == "none" else g * (0.8 * (u * um + (1 + u) * Em) + ACT) + 2 * F32 * np.abs(du)
+    g, Em = (np.abs(O.merge_heads(v, H)) for v in (hd, Eu))
+    Edu = np.zeros_like(du) if act == "none" else g * (0.8 * Em + ACT) + 2 * F32 * np.abs(du)
     Eb = Edu.sum((0, 1)) + (B * T + 2) * F32 * (np.abs(du) + Edu).sum((0, 1))
     within(db, wb, Eb, "db")
     Er = Edu + (u * (np.abs(du) + Edu) if act != "none" else 0.0)   # rounded as an operand
