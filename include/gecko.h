@@ -393,7 +393,7 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
  *   dstate_out     : [B, D] fp32 gradient of state_out, or NULL for zero.
  *   dstate_in      : [B, D] fp32, or NULL; may equal dstate_out.
  */
-#define GECKO_SCAN_CHUNK 256
+#define GECKO_SCAN_CHUNK 128
 int gecko_gated_scan_workspace(int64_t B, int64_t L, int64_t D, int dtype, int backward, int64_t* bytes);
 int gecko_gated_scan_forward(const void* x, const void* log_a, void* y, const uint8_t* reset, const float* state_in,
                              float* state_out, float* chunk_state, int64_t B, int64_t L, int64_t D, int dtype,

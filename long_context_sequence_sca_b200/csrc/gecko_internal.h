@@ -205,7 +205,7 @@ cudaError_t launch_tdnorm(const NormProblem& p, const NormWorkspace& w, cudaStre
 
 // Tokens per chunk of the gated scan: the spacing of the states that the
 // forward keeps for the backward.
-constexpr int kScanChunk = 256;
+constexpr int kScanChunk = 128;
 inline int64_t scan_chunks(int64_t L) { return (L + kScanChunk - 1) / kScanChunk; }
 
 // One validated call: x, log_a [B, L, D] (dtype); reset [B, L] uint8 or null.

@@ -9,7 +9,7 @@
 // Everything is held in fp32 whatever the tensors' type.
 //
 // The work is bound by HBM (3 values per element forward, 5 backward), so a
-// tile of one chunk (256 tokens) by 128 bytes of features is read once, by TMA,
+// tile of one chunk (128 tokens) by 128 bytes of features is read once, by TMA,
 // into shared memory and scanned there: warp w takes tokens 32 w .. 32 w + 31,
 // a lane the features of 4 bytes.  First every warp finds the map of its span,
 // then the state entering the chunk is fetched, then every warp scans again
@@ -20,14 +20,15 @@
 // state entering its group of 16 chunks and the maps of the chunks between, so
 // the chain of dependent hand-offs is 16 times shorter than the chain of
 // chunks, and the association, and with it every bit of the result, does not
-// depend on timing.
+// depend on timing.  What is published is its own flag: the memory starts as
+// all ones, a pattern that no result has.
 #include "common.cuh"
 #include "gecko_internal.h"
 
 namespace gecko {
 namespace {
 
-constexpr int kWarps = 8, kSpan = kScanChunk / kWarps;   // tokens per warp: 32, one reset bit each in a word
+constexpr int kWarps = 4, kSpan = kScanChunk / kWarps;   // tokens per warp: 32, one reset bit each in a word
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;                               // chunks per group of the hand-off
 constexpr int kRowBytes = 128;                           // features per tile, in bytes
@@ -66,11 +67,11 @@ struct ScanArgs {
   float* chunk_state;     // [B, C, D]
   int64_t L, D;
   int B, C, tiles;        // tiles of features
-  // hand-off (ws): [0] the counter, [1] the abort flag, then one flag per
-  // (b, tile, chunk of the walk); maps (A, h) [B, C, D]; group states [B, G, D]
+  // hand-off (ws, all ones at the start): [0] the counter, [1] set if a block
+  // gave up; maps (A, h) [B, C, D]; group states [B, G, D]
   int* sync;
-  float2* map;
-  float* group;
+  uint64_t* map;
+  uint32_t* group;
   int* status;
 };
 
@@ -78,17 +79,65 @@ struct Tile {
   int c, b, tile;   // chunk along the walk
 };
 
-__device__ __forceinline__ int load_acquire(const int* p) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+// Published values: single 64-bit (a map) or 32-bit (a state) words, several of
+// them with one access; a word that still is all ones is not there yet.
+constexpr uint64_t kNoMap = ~0ull;
+constexpr uint32_t kNoState = ~0u;
+
+__device__ __forceinline__ void publish(uint64_t* p, const uint64_t (&v)[2]) {
+  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(v[0]), "l"(v[1]) : "memory");
 }
-__device__ __forceinline__ void store_release(int* p, int v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void publish(uint64_t* p, const uint64_t (&v)[1]) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v[0]) : "memory");
+}
+__device__ __forceinline__ void publish(uint32_t* p, const uint32_t (&v)[2]) {
+  asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(v[0]), "r"(v[1]) : "memory");
+}
+__device__ __forceinline__ void publish(uint32_t* p, const uint32_t (&v)[1]) {
+  asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v[0]) : "memory");
+}
+__device__ __forceinline__ void peek(const uint64_t* p, uint64_t (&v)[2]) {
+  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void peek(const uint64_t* p, uint64_t (&v)[1]) {
+  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v[0]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void peek(const uint32_t* p, uint32_t (&v)[2]) {
+  asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void peek(const uint32_t* p, uint32_t (&v)[1]) {
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v[0]) : "l"(p) : "memory");
 }
 
-__device__ __forceinline__ int* flag_of(const ScanArgs& a, const Tile& t, int c) {
-  return a.sync + 2 + ((int64_t)t.b * a.tiles + t.tile) * a.C + c;
+// (A, h) as one word.  Arithmetic gives no NaN of all ones; one that an input
+// carried through is stored as another NaN.
+__device__ __forceinline__ uint32_t not_ones(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u == ~0u ? 0x7fffffffu : u;
+}
+__device__ __forceinline__ uint64_t map_word(float A, float h) {
+  return (uint64_t)not_ones(h) << 32 | not_ones(A);
+}
+
+// Repeat `look` (true: all there) until it holds for the whole warp.  False if
+// that takes longer than the wait limit, or another block gave up.
+template <class Look>
+__device__ __forceinline__ bool wait_for(const ScanArgs& a, Look&& look) {
+  if (__all_sync(0xffffffffu, look())) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, look())) return true;
+    if ((it & 63u) == 0) {
+      const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(a.sync + 1) == 1)) {
+        if ((threadIdx.x & 31) == 0) {
+          *reinterpret_cast<volatile int*>(a.sync + 1) = 1;
+          atomicOr(a.status, kStatusTimeout);
+        }
+        return false;
+      }
+    }
+  }
 }
 
 // One warp: publish the chunk's map, wait for what precedes it, and return the
@@ -97,83 +146,73 @@ __device__ __forceinline__ int* flag_of(const ScanArgs& a, const Tile& t, int c)
 template <int V>
 __device__ __forceinline__ bool hand_off(const ScanArgs& a, const Tile& t, int64_t d, bool on, const float (&A)[V],
                                          const float (&m)[V], float (&h)[V]) {
-  const int lane = threadIdx.x & 31;
   const int first = t.c / kGroup * kGroup, n = t.c - first;   // chunks of the group before this one
-  const bool last_of_group = n == kGroup - 1 && t.c + 1 < a.C;
-  const int64_t row = (int64_t)t.b * a.C;
-  if (n < kGroup - 1 && t.c + 1 < a.C) {
-    if (on)
+  const bool last = t.c + 1 == a.C;
+  const int64_t G = (a.C + kGroup - 1) / kGroup;
+  uint64_t* map = a.map + ((int64_t)t.b * a.C + t.c) * a.D + d;
+  uint32_t* group = a.group + ((int64_t)t.b * G + first / kGroup) * a.D + d;
+  if (on && n < kGroup - 1 && !last) {
+    uint64_t w[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) __stcg(a.map + (row + t.c) * a.D + d + i, make_float2(A[i], m[i]));
-    __syncwarp();
-    if (lane == 0) {
-      __threadfence();
-      store_release(flag_of(a, t, t.c), 1);
-    }
+    for (int i = 0; i < V; ++i) w[i] = map_word(A[i], m[i]);
+    publish(map, w);
   }
-  // lane l < n: the map of chunk first + l; lane 31: the state entering the group
-  const int* want = lane < n ? flag_of(a, t, first + lane) : lane == 31 && first ? flag_of(a, t, first - 1) : nullptr;
-  bool ready = !want || load_acquire(want) != 0;
-  if (!__all_sync(0xffffffffu, ready)) {
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-      if (!ready) ready = load_acquire(want) != 0;
-      if (__all_sync(0xffffffffu, ready)) break;
-      if ((it & 63u) == 0) {
-        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
-        if (__any_sync(0xffffffffu, late || load_acquire(a.sync + 1))) {
-          if (lane == 0) {
-            store_release(a.sync + 1, 1);
-            atomicOr(a.status, kStatusTimeout);
-          }
-          return false;
-        }
-      }
-    }
-  }
-  __syncwarp();
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = 0.f;
-  if (on) {
-    const int64_t bd = (int64_t)t.b * a.D + d;
-    if (first) {
-      const int64_t G = (a.C + kGroup - 1) / kGroup;
+  if (first) {
+    uint32_t w[V];
+    if (!wait_for(a, [&] {
+          if (!on) return true;
+          peek(group, w);
+          bool there = true;
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = __ldcg(a.group + ((int64_t)t.b * G + first / kGroup) * a.D + d + i);
-    } else if (a.enter0) {
+          for (int i = 0; i < V; ++i) there &= w[i] != kNoState;
+          return there;
+        }))
+      return false;
+    if (on)
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = a.enter0[t.b * a.enter0_stride + d + i];
-    }
-    // loads five ahead of their folds (all fifteen would spill)
+      for (int i = 0; i < V; ++i) h[i] = __uint_as_float(w[i]);
+  } else if (on && a.enter0) {
 #pragma unroll
-    for (int c0 = 0; c0 < kGroup - 1; c0 += 5) {
-      float2 am[5][V];
-#pragma unroll
-      for (int c = 0; c < 5; ++c)
-        if (c0 + c < n)
-#pragma unroll
-          for (int i = 0; i < V; ++i) am[c][i] = __ldcg(a.map + (row + first + c0 + c) * a.D + d + i);
-#pragma unroll
-      for (int c = 0; c < 5; ++c)
-        if (c0 + c < n)
-#pragma unroll
-          for (int i = 0; i < V; ++i) h[i] = decay_fma(am[c][i].x, h[i], am[c][i].y);
-    }
-    if (last_of_group) {
-      const int64_t G = (a.C + kGroup - 1) / kGroup;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        __stcg(a.group + ((int64_t)t.b * G + first / kGroup + 1) * a.D + d + i, decay_fma(A[i], h[i], m[i]));
-    }
-    if (t.c + 1 == a.C && a.leave) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) a.leave[bd + i] = decay_fma(A[i], h[i], m[i]);
-    }
+    for (int i = 0; i < V; ++i) h[i] = a.enter0[t.b * a.enter0_stride + d + i];
   }
-  __syncwarp();
-  if (last_of_group && lane == 0) {
-    __threadfence();
-    store_release(flag_of(a, t, t.c), 1);
+  // loads five ahead of their folds (all fifteen would spill)
+#pragma unroll
+  for (int c0 = 0; c0 < kGroup - 1; c0 += 5) {
+    if (c0 >= n) break;
+    uint64_t w[5][V];
+    if (!wait_for(a, [&] {
+          if (!on) return true;
+#pragma unroll
+          for (int c = 0; c < 5; ++c)
+            if (c0 + c < n) peek(map - (int64_t)(n - c0 - c) * a.D, w[c]);
+          bool there = true;
+#pragma unroll
+          for (int c = 0; c < 5; ++c)
+            if (c0 + c < n)
+#pragma unroll
+              for (int i = 0; i < V; ++i) there &= w[c][i] != kNoMap;
+          return there;
+        }))
+      return false;
+    if (on)
+#pragma unroll
+      for (int c = 0; c < 5; ++c)
+        if (c0 + c < n)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            h[i] = decay_fma(__uint_as_float((uint32_t)w[c][i]), h[i], __uint_as_float((uint32_t)(w[c][i] >> 32)));
+  }
+  if (on && n == kGroup - 1 && !last) {
+    uint32_t w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = not_ones(decay_fma(A[i], h[i], m[i]));
+    publish(group + a.D, w);
+  }
+  if (on && last && a.leave) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.leave[(int64_t)t.b * a.D + d + i] = decay_fma(A[i], h[i], m[i]);
   }
   return true;
 }
@@ -190,7 +229,7 @@ struct ScanSmem {
 // Which tile this block takes: drawn from the counter, or (one chunk: nothing
 // to wait for) the block's own index.
 __device__ __forceinline__ Tile draw_tile(const ScanArgs& a, int* slot) {
-  if (threadIdx.x == 0) *slot = a.C > 1 ? atomicAdd(a.sync, 1) : (int)blockIdx.x;
+  if (threadIdx.x == 0) *slot = a.C > 1 ? atomicAdd(a.sync, 1) + 1 : (int)blockIdx.x;   // counts from -1
   __syncthreads();
   const int u = *slot, per_chunk = a.B * a.tiles;
   Tile t;
@@ -230,7 +269,7 @@ __device__ __forceinline__ void fold(const float2 (&map)[kWarps][F], int f, int 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) scan_kernel(const __grid_constant__ CUtensorMap mx,
+__global__ void __launch_bounds__(kThreads, 6) scan_kernel(const __grid_constant__ CUtensorMap mx,
                                                            const __grid_constant__ CUtensorMap mg,
                                                            const __grid_constant__ CUtensorMap my, const ScanArgs a) {
   constexpr int V = kV<T>, F = kFT<T>;
@@ -320,8 +359,9 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const __grid_constant
 
 // A few tokens (generation): no tile to fill, a thread walks over the tokens of
 // four features.  Measured, this takes 1.5 us + 0.23 us a token, the chunk
-// kernel 6.2 us + 0.014 us a tile (1 to 256 tokens of 512 to 131072 features).
-bool short_is_faster(int64_t L, int64_t tiles) { return L <= 128 && L <= 20 + tiles / 16; }
+// kernel 5 us and, beyond 64 tiles, about 0.008 us a tile more (1 to 128 tokens
+// of 512 to 131072 features); past 64 tokens its strided rows lose to TMA's.
+bool short_is_faster(int64_t L, int64_t tiles) { return L <= 64 && L <= 16 + tiles / 64; }
 
 template <typename T>
 struct alignas(4 * sizeof(T)) Four {
@@ -364,7 +404,7 @@ __global__ void __launch_bounds__(128) scan_short_kernel(const T* x, const T* lo
 // e = sum_t P_t dy_t + P e_next.  Then it scans forward again, keeping the 32
 // states h_{t-1} in registers, and back over them.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const __grid_constant__ CUtensorMap mx,
+__global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_constant__ CUtensorMap mx,
                                                                const __grid_constant__ CUtensorMap mg,
                                                                const __grid_constant__ CUtensorMap mdy,
                                                                const __grid_constant__ CUtensorMap mdx,
@@ -502,7 +542,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [B, L, D] as a 3D map {D, L, B}, box {128 bytes of features, 256, 1}.
+// [B, L, D] as a 3D map {D, L, B}, box {128 bytes of features, 128, 1}.
 template <typename T>
 bool make_map(CUtensorMap* m, const void* base, const ScanProblem& p) {
   EncodeTiledFn fn = encode_fn();
@@ -524,13 +564,11 @@ int64_t tiles_of(int64_t D, int dtype) {
   const int64_t ft = dtype == kBF16 ? kFT<__nv_bfloat16> : kFT<float>;
   return (D + ft - 1) / ft;
 }
-size_t sync_bytes(int64_t B, int64_t L, int64_t D, int dtype) {
-  return up256(sizeof(int) * (2 + (size_t)(B * tiles_of(D, dtype) * scan_chunks(L))));
-}
+constexpr size_t kSyncBytes = 256;
 int64_t groups_of(int64_t L) { return (scan_chunks(L) + kGroup - 1) / kGroup; }
 
 // Fill the arguments, enter and leave being the states at the walk's ends, and
-// clear the hand-off's flags.  The last chunk may be done before others of the
+// set the hand-off's memory to all ones.  The last chunk may be done before others of the
 // first group have read the entering state, so if it is to be overwritten
 // they read a copy (in the slot of the first group's state).
 cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, ScanArgs* a, cudaStream_t st) {
@@ -544,22 +582,23 @@ cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, Sca
   a->status = p.status;
   char* ws = static_cast<char*>(p.ws);
   a->sync = reinterpret_cast<int*>(ws);
-  const size_t sb = sync_bytes(p.B, p.L, p.D, p.dtype);
-  a->map = reinterpret_cast<float2*>(ws + sb);
-  a->group = reinterpret_cast<float*>(ws + sb + up256(sizeof(float2) * p.B * a->C * p.D));
+  const size_t map_bytes = up256(sizeof(uint64_t) * p.B * a->C * p.D);
+  a->map = reinterpret_cast<uint64_t*>(ws + kSyncBytes);
+  a->group = reinterpret_cast<uint32_t*>(ws + kSyncBytes + map_bytes);
   a->enter0 = enter;
   a->enter0_stride = p.D;
   a->leave = leave;
   if (a->C == 1) return cudaSuccess;
+  if (cudaError_t e = cudaMemsetAsync(ws, 0xff, scan_workspace_bytes(p.B, p.L, p.D, p.dtype, false), st)) return e;
   if (enter && enter == leave) {
-    a->enter0 = a->group;
+    a->enter0 = reinterpret_cast<float*>(a->group);
     a->enter0_stride = groups_of(p.L) * p.D;
     const size_t row = sizeof(float) * p.D;
     if (cudaError_t e = cudaMemcpy2DAsync(a->group, row * groups_of(p.L), enter, row, row, p.B,
                                           cudaMemcpyDeviceToDevice, st))
       return e;
   }
-  return cudaMemsetAsync(ws, 0, sb, st);
+  return cudaSuccess;
 }
 
 template <typename T>
@@ -609,10 +648,10 @@ bool scan_grid_fits(int64_t B, int64_t L, int64_t D, int dtype) {
   return (long double)B * tiles_of(D, dtype) * scan_chunks(L) < 2147483647.0L && (long double)L * D < 2.0e11L;
 }
 
-size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int dtype, bool) {
+size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int, bool) {
   if (scan_chunks(L) == 1) return 0;
-  return sync_bytes(B, L, D, dtype) + up256(sizeof(float2) * (size_t)(B * scan_chunks(L) * D)) +
-         up256(sizeof(float) * (size_t)(B * groups_of(L) * D));
+  return kSyncBytes + up256(sizeof(uint64_t) * (size_t)(B * scan_chunks(L) * D)) +
+         up256(sizeof(uint32_t) * (size_t)(B * groups_of(L) * D));
 }
 
 cudaError_t launch_scan(const ScanProblem& p, cudaStream_t st) {

@@ -528,7 +528,7 @@ def tdnorm_forward(x, gamma, bias, G: int, beta1: float, beta2: float, eps: floa
 
 # -------------------------------------------- layer steps around the path --
 
-SCAN_CHUNK = 256
+SCAN_CHUNK = 128
 ACTS = {"none": 0, "silu": 1, "gelu": 2}
 
 
@@ -606,7 +606,7 @@ def gated_scan_forward(x, log_a, reset=None, state_in=None, return_state=False, 
     """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t over x, log_a
     [B, L, D] (float32 or bfloat16).  reset: [B, L] uint8 or None; state_in:
     [B, D] float32 or None.  Returns y, followed by the final state [B, D] if
-    return_state and by the chunk states [B, ceil(L / 256), D] that
+    return_state and by the chunk states [B, ceil(L / 128), D] that
     gated_scan_backward needs if keep_chunks.  y may be x."""
     _main(x, "x")
     B, L, D = x.shape
