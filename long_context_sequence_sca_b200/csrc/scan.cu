@@ -39,25 +39,71 @@ static_assert(kSpan == 32, "a span's document starts are one 32-bit word");
 template <typename T> constexpr int kV = 4 / (int)sizeof(T);
 template <typename T> constexpr int kFT = 32 * kV<T>;
 
-__device__ __forceinline__ void read4(const uint8_t* p, float (&v)[2]) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-  v[0] = __uint_as_float(u << 16);
-  v[1] = __uint_as_float(u & 0xffff0000u);
+// The features of one lane: one fp32 value, or two, bf16 in memory and a packed
+// pair in arithmetic.
+template <typename T> struct Lane;
+template <> struct Lane<float> {
+  using Raw = float;
+  using Val = float;
+  static __device__ __forceinline__ Val open(Raw r) { return r; }
+  static __device__ __forceinline__ Raw shut(Val v) { return v; }
+  static __device__ __forceinline__ Val all(float v) { return v; }
+  static __device__ __forceinline__ Val fma(Val a, Val b, Val c) { return fmaf(a, b, c); }
+  static __device__ __forceinline__ Val mul(Val a, Val b) { return a * b; }
+  static __device__ __forceinline__ Val add(Val a, Val b) { return a + b; }
+  static __device__ __forceinline__ void get(Val v, float (&f)[1]) { f[0] = v; }
+  static __device__ __forceinline__ Val put(const float (&f)[1]) { return f[0]; }
+  static __device__ __forceinline__ Raw least(Raw a, Raw b) { return fminf(a, b); }
+  static __device__ __forceinline__ float lowest(Raw r) { return r; }
+  // The full expf: its error stays at 2^-23 however many tokens multiply it.
+  static __device__ __forceinline__ Val gate(Val log_a) { return expf(log_a); }
+};
+template <> struct Lane<__nv_bfloat16> {
+  using Raw = uint32_t;
+  using Val = uint64_t;
+  static __device__ __forceinline__ Val open(Raw r) {
+    return pack2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  }
+  static __device__ __forceinline__ Raw shut(Val v) {
+    float f[2];
+    unpack2(v, f[0], f[1]);
+    return pack_bf16x2(f[0], f[1]);
+  }
+  static __device__ __forceinline__ Val all(float v) { return pack2(v, v); }
+  static __device__ __forceinline__ Val fma(Val a, Val b, Val c) { return ffma2(a, b, c); }
+  static __device__ __forceinline__ Val mul(Val a, Val b) { return fmul2(a, b); }
+  static __device__ __forceinline__ Val add(Val a, Val b) { return fadd2(a, b); }
+  static __device__ __forceinline__ void get(Val v, float (&f)[2]) { unpack2(v, f[0], f[1]); }
+  static __device__ __forceinline__ Val put(const float (&f)[2]) { return pack2(f[0], f[1]); }
+  static __device__ __forceinline__ Raw least(Raw a, Raw b) {
+    const __nv_bfloat162 m = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const Raw*>(&m);
+  }
+  static __device__ __forceinline__ float lowest(Raw r) {
+    return fminf(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  }
+  // The SFU's 2^x: 2^-22 relative, and |log_a| 2^-24 from the scaled argument.
+  static __device__ __forceinline__ Val gate(Val log_a) {
+    float f[2];
+    unpack2(fmul2(log_a, pack2(kLog2e, kLog2e)), f[0], f[1]);
+    return pack2(ex2(f[0]), ex2(f[1]));
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ typename Lane<T>::Raw read4(const uint8_t* p) {
+  return *reinterpret_cast<const typename Lane<T>::Raw*>(p);
 }
-__device__ __forceinline__ void read4(const uint8_t* p, float (&v)[1]) { v[0] = *reinterpret_cast<const float*>(p); }
-__device__ __forceinline__ void write4(uint8_t* p, const float (&v)[2]) {
-  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+template <typename T>
+__device__ __forceinline__ void write4(uint8_t* p, typename Lane<T>::Raw v) {
+  *reinterpret_cast<typename Lane<T>::Raw*>(p) = v;
 }
-__device__ __forceinline__ void write4(uint8_t* p, const float (&v)[1]) { *reinterpret_cast<float*>(p) = v[0]; }
 
 // A decay of zero drops what came before, even if that is not finite.
 __device__ __forceinline__ float decay_fma(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
 
-// exp(log_a): for bf16 gates the SFU's 2^x (2^-22 relative, and |log_a| 2^-24
-// from the scaled argument); fp32 gates take the full expf, whose error stays
-// at 2^-23 however many tokens multiply it.
-__device__ __forceinline__ float gate(float log_a, __nv_bfloat16) { return ex2(log_a * kLog2e); }
-__device__ __forceinline__ float gate(float log_a, float) { return expf(log_a); }
+// log_a above this: the gate is not zero.
+constexpr float kOpen = -87.f;
 
 struct ScanArgs {
   const uint8_t* reset;
@@ -247,12 +293,119 @@ __device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int b, int64_t
   return __ballot_sync(0xffffffffu, start);
 }
 
-// The gates of token s of a span.
-template <typename T>
-__device__ __forceinline__ void gates(const uint8_t* row, uint32_t starts, int s, float (&a)[kV<T>]) {
-  read4(row, a);
+// One token's gates.  kShut: some gate of the span may be zero (a document
+// starts there, or log_a is low enough), and what a zero gate meets is dropped;
+// otherwise the products are taken as they are, two features at a time.
+template <typename T, bool kShut>
+__device__ __forceinline__ typename Lane<T>::Val gate_at(typename Lane<T>::Raw raw, uint32_t starts, int s) {
+  using X = Lane<T>;
+  const typename X::Val g = X::gate(X::open(raw));
+  return kShut && (starts >> s & 1u) ? X::all(0.f) : g;
+}
+
+// a h + x, x where a is zero.
+template <typename T, bool kShut>
+__device__ __forceinline__ typename Lane<T>::Val step(typename Lane<T>::Val a, typename Lane<T>::Val h,
+                                                      typename Lane<T>::Val x) {
+  using X = Lane<T>;
+  if (!kShut) return X::fma(a, h, x);
+  float av[kV<T>], hv[kV<T>], xv[kV<T>];
+  X::get(a, av);
+  X::get(h, hv);
+  X::get(x, xv);
 #pragma unroll
-  for (int i = 0; i < kV<T>; ++i) a[i] = starts >> s & 1u ? 0.f : gate(a[i], T());
+  for (int i = 0; i < kV<T>; ++i) hv[i] = decay_fma(av[i], hv[i], xv[i]);
+  return X::put(hv);
+}
+
+// a b, 0 where a is zero.
+template <typename T, bool kShut>
+__device__ __forceinline__ typename Lane<T>::Val times(typename Lane<T>::Val a, typename Lane<T>::Val b) {
+  using X = Lane<T>;
+  if (!kShut) return X::mul(a, b);
+  float av[kV<T>], bv[kV<T>];
+  X::get(a, av);
+  X::get(b, bv);
+#pragma unroll
+  for (int i = 0; i < kV<T>; ++i) bv[i] = av[i] == 0.f ? 0.f : av[i] * bv[i];
+  return X::put(bv);
+}
+
+// The map of a span: A the product of its gates, h its scan from zero; for the
+// backward also e, what the span passes back of its own output gradients.
+// Returns the lowest log_a.  Tokens past the end read as zeros: a = 1, x = 0,
+// the identity.
+template <typename T, bool kShut, bool kBack>
+__device__ __forceinline__ float span_map(const uint8_t* pg, const uint8_t* px, const uint8_t* pd, uint32_t starts,
+                                          typename Lane<T>::Val& A, typename Lane<T>::Val& h,
+                                          typename Lane<T>::Val& e) {
+  using X = Lane<T>;
+  A = X::all(1.f);
+  h = e = X::all(0.f);
+  typename X::Raw low = read4<T>(pg);
+#pragma unroll 8
+  for (int s = 0; s < kSpan; ++s) {
+    const typename X::Raw raw = read4<T>(pg + s * kRowBytes);
+    low = X::least(low, raw);
+    const typename X::Val g = gate_at<T, kShut>(raw, starts, s);
+    h = step<T, kShut>(g, h, X::open(read4<T>(px + s * kRowBytes)));
+    A = X::mul(A, g);
+    if (kBack) e = X::add(e, times<T, kShut>(A, X::open(read4<T>(pd + s * kRowBytes))));
+  }
+  return X::lowest(low);
+}
+
+// Whether the careful form is needed, decided for the warp; the map that goes
+// with it.
+template <typename T, bool kBack>
+__device__ __forceinline__ bool span_map_of(const uint8_t* pg, const uint8_t* px, const uint8_t* pd, uint32_t starts,
+                                            typename Lane<T>::Val& A, typename Lane<T>::Val& h,
+                                            typename Lane<T>::Val& e) {
+  if (!starts && __all_sync(0xffffffffu, span_map<T, false, kBack>(pg, px, pd, 0, A, h, e) > kOpen)) return false;
+  span_map<T, true, kBack>(pg, px, pd, starts, A, h, e);
+  return true;
+}
+
+// y over the consumed x.
+template <typename T, bool kShut>
+__device__ __forceinline__ void span_out(const uint8_t* pg, uint8_t* px, uint32_t starts, typename Lane<T>::Val h) {
+  using X = Lane<T>;
+#pragma unroll 8
+  for (int s = 0; s < kSpan; ++s) {
+    const typename X::Val g = gate_at<T, kShut>(read4<T>(pg + s * kRowBytes), starts, s);
+    h = step<T, kShut>(g, h, X::open(read4<T>(px + s * kRowBytes)));
+    write4<T>(px + s * kRowBytes, X::shut(h));
+  }
+}
+
+// The states h_{t-1} of a span.
+template <typename T, bool kShut>
+__device__ __forceinline__ void span_states(const uint8_t* pg, const uint8_t* px, uint32_t starts,
+                                            typename Lane<T>::Val h, typename Lane<T>::Val (&before)[kSpan]) {
+  using X = Lane<T>;
+#pragma unroll
+  for (int s = 0; s < kSpan; ++s) {
+    before[s] = h;
+    const typename X::Val g = gate_at<T, kShut>(read4<T>(pg + s * kRowBytes), starts, s);
+    h = step<T, kShut>(g, h, X::open(read4<T>(px + s * kRowBytes)));
+  }
+}
+
+// dx over dy, dlog_a over log_a.
+template <typename T, bool kShut>
+__device__ __forceinline__ void span_back(uint8_t* pg, uint8_t* pd, uint32_t starts, typename Lane<T>::Val e,
+                                          const typename Lane<T>::Val (&before)[kSpan]) {
+  using X = Lane<T>;
+#pragma unroll
+  for (int s = kSpan - 1; s >= 0; --s) {
+    const typename X::Val g = gate_at<T, kShut>(read4<T>(pg + s * kRowBytes), starts, s);
+    const typename X::Val dh = X::add(X::open(read4<T>(pd + s * kRowBytes)), e);
+    e = times<T, kShut>(g, dh);
+    // (where the gate is zero e is, and before may not be finite)
+    const typename X::Val dg = times<T, kShut>(e, before[s]);
+    write4<T>(pd + s * kRowBytes, X::shut(dh));
+    write4<T>(pg + s * kRowBytes, X::shut(dg));
+  }
 }
 
 // Map of the chunk and, for this thread's span, of what precedes it in the chunk.
@@ -298,22 +451,14 @@ __global__ void __launch_bounds__(kThreads, 6) scan_kernel(const __grid_constant
   }
   uint8_t *px = tx + warp * kSpan * kRowBytes + lane * 4, *pg = tg + warp * kSpan * kRowBytes + lane * 4;
   const int f = lane * V;
+  using X = Lane<T>;
+  bool shut;
   {
-    // tokens past the end read as zeros: a = 1, x = 0, the identity
+    typename X::Val Av, hv, ev;
+    shut = span_map_of<T, false>(pg, px, nullptr, starts, Av, hv, ev);
     float A[V], h[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 1.f, h[i] = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < kSpan; ++s) {
-      float g[V], x[V];
-      gates<T>(pg + s * kRowBytes, starts, s, g);
-      read4(px + s * kRowBytes, x);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        h[i] = decay_fma(g[i], h[i], x[i]);
-        A[i] *= g[i];
-      }
-    }
+    X::get(Av, A);
+    X::get(hv, h);
 #pragma unroll
     for (int i = 0; i < V; ++i) sm.map[warp][f + i] = make_float2(A[i], h[i]);
   }
@@ -339,15 +484,8 @@ __global__ void __launch_bounds__(kThreads, 6) scan_kernel(const __grid_constant
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = sm.enter[f + i], A[i] = 1.f;
   fold<V, F>(sm.map, f, 0, warp, 1, A, h);
-#pragma unroll 8
-  for (int s = 0; s < kSpan; ++s) {
-    float g[V], x[V];
-    gates<T>(pg + s * kRowBytes, starts, s, g);
-    read4(px + s * kRowBytes, x);
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = decay_fma(g[i], h[i], x[i]);
-    write4(px + s * kRowBytes, h);   // y over the consumed x
-  }
+  if (shut) span_out<T, true>(pg, px, starts, X::put(h));
+  else span_out<T, false>(pg, px, starts, X::put(h));
   fence_proxy_async_smem();
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -367,6 +505,12 @@ template <typename T>
 struct alignas(4 * sizeof(T)) Four {
   T v[4];
 };
+
+// The same gates as the chunk kernel's.
+template <typename T>
+__device__ __forceinline__ float gate1(float log_a) {
+  return sizeof(T) == 2 ? ex2(log_a * kLog2e) : expf(log_a);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(128) scan_short_kernel(const T* x, const T* log_a, T* y, const float* state_in,
@@ -390,7 +534,7 @@ __global__ void __launch_bounds__(128) scan_short_kernel(const T* x, const T* lo
     Four<T> o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      h[j] = decay_fma(start ? 0.f : gate(to_f32(g.v[j]), T()), h[j], to_f32(u.v[j]));
+      h[j] = decay_fma(start ? 0.f : gate1<T>(to_f32(g.v[j])), h[j], to_f32(u.v[j]));
       o.v[j] = from_f32<T>(h[j]);
     }
     *reinterpret_cast<Four<T>*>(y + at + t * a.D) = o;
@@ -443,23 +587,15 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_cons
   }
   const int off = warp * kSpan * kRowBytes + lane * 4;
   uint8_t *px = tx + off, *pg = tg + off, *pd = td + off;
+  using X = Lane<T>;
+  bool shut;
   {
+    typename X::Val Pv, hv, ev;
+    shut = span_map_of<T, true>(pg, px, pd, starts, Pv, hv, ev);
     float P[V], h[V], e[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) P[i] = 1.f, h[i] = e[i] = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < kSpan; ++s) {
-      float g[V], x[V], dy[V];
-      gates<T>(pg + s * kRowBytes, starts, s, g);
-      read4(px + s * kRowBytes, x);
-      read4(pd + s * kRowBytes, dy);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        h[i] = decay_fma(g[i], h[i], x[i]);
-        P[i] *= g[i];
-        e[i] = P[i] == 0.f ? e[i] : fmaf(P[i], dy[i], e[i]);
-      }
-    }
+    X::get(Pv, P);
+    X::get(hv, h);
+    X::get(ev, e);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       sm.map[warp][f + i] = make_float2(P[i], h[i]);
@@ -482,38 +618,17 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = h0[i], A[i] = 1.f;
   fold<V, F>(sm.map, f, 0, warp, 1, A, h);
-  float before[kSpan][V];
-#pragma unroll
-  for (int s = 0; s < kSpan; ++s) {
-    float g[V], x[V];
-    gates<T>(pg + s * kRowBytes, starts, s, g);
-    read4(px + s * kRowBytes, x);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      before[s][i] = h[i];
-      h[i] = decay_fma(g[i], h[i], x[i]);
-    }
-  }
+  typename X::Val before[kSpan];
+  if (shut) span_states<T, true>(pg, px, starts, X::put(h), before);
+  else span_states<T, false>(pg, px, starts, X::put(h), before);
   __syncthreads();
   if (!sm.ok) return;
   float e[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) e[i] = sm.enter_back[f + i];
   fold<V, F>(sm.back, f, kWarps - 1, warp, -1, A, e);
-#pragma unroll
-  for (int s = kSpan - 1; s >= 0; --s) {
-    float g[V], dh[V], dg[V];
-    gates<T>(pg + s * kRowBytes, starts, s, g);
-    read4(pd + s * kRowBytes, dh);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      dh[i] += e[i];
-      e[i] = g[i] == 0.f ? 0.f : g[i] * dh[i];
-      dg[i] = g[i] == 0.f ? 0.f : e[i] * before[s][i];
-    }
-    write4(pd + s * kRowBytes, dh);   // dx over dy, dlog_a over log_a
-    write4(pg + s * kRowBytes, dg);
-  }
+  if (shut) span_back<T, true>(pg, pd, starts, X::put(e), before);
+  else span_back<T, false>(pg, pd, starts, X::put(e), before);
   fence_proxy_async_smem();
   __syncthreads();
   if (threadIdx.x == 0) {
