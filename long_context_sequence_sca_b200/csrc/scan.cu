@@ -186,91 +186,113 @@ __device__ __forceinline__ bool wait_for(const ScanArgs& a, Look&& look) {
   }
 }
 
-// One warp: publish the chunk's map, wait for what precedes it, and return the
-// state entering the chunk in h; publish the state entering the next group.
-// False if a wait ran out.
+template <typename T, bool kBack>
+struct ScanSmem {
+  float2 map[kWarps][kFT<T>];    // (A, h) of every warp's span
+  float2 back[kBack ? kWarps : 1][kBack ? kFT<T> : 1];   // the same of the reverse recurrence
+  float2 pre[kWarps][kFT<T>];    // the maps of the group's earlier chunks, a quarter of them each
+  float enter[kFT<T>];           // the state entering the group
+  uint64_t bar;
+  int abort_flag, unit;
+};
+
+// One lane's place in the hand-off.
 template <int V>
-__device__ __forceinline__ bool hand_off(const ScanArgs& a, const Tile& t, int64_t d, bool on, const float (&A)[V],
-                                         const float (&m)[V], float (&h)[V]) {
-  const int first = t.c / kGroup * kGroup, n = t.c - first;   // chunks of the group before this one
-  const bool last = t.c + 1 == a.C;
+struct Place {
+  int first, n;       // the group's first chunk; its chunks before this one
+  bool last, on;
+  uint64_t* map;      // of this chunk
+  uint32_t* group;    // of this group
+  int64_t d;
+};
+template <int V>
+__device__ __forceinline__ Place<V> place_of(const ScanArgs& a, const Tile& t, int64_t d) {
+  Place<V> p;
+  p.first = t.c / kGroup * kGroup;
+  p.n = t.c - p.first;
+  p.last = t.c + 1 == a.C;
+  p.on = d < a.D;
+  p.d = d;
   const int64_t G = (a.C + kGroup - 1) / kGroup;
-  uint64_t* map = a.map + ((int64_t)t.b * a.C + t.c) * a.D + d;
-  uint32_t* group = a.group + ((int64_t)t.b * G + first / kGroup) * a.D + d;
-  if (on && n < kGroup - 1 && !last) {
-    uint64_t w[V];
+  p.map = a.map + ((int64_t)t.b * a.C + t.c) * a.D + d;
+  p.group = a.group + ((int64_t)t.b * G + p.first / kGroup) * a.D + d;
+  return p;
+}
+
+// The chunk's map for the chunks of the group that come after it.
+template <int V>
+__device__ __forceinline__ void publish_map(const Place<V>& p, const float (&A)[V], const float (&m)[V]) {
+  if (!p.on || p.last || p.n == kGroup - 1) return;
+  uint64_t w[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[i] = map_word(A[i], m[i]);
-    publish(map, w);
+  for (int i = 0; i < V; ++i) w[i] = map_word(A[i], m[i]);
+  publish(p.map, w);
+}
+
+// Every warp: wait for a quarter of the group's earlier maps and compose them;
+// warp 0 also for the state entering the group.  All of them are asked for at
+// once, so the hand-off costs one trip to the L2.  False if the wait ran out.
+template <int V, class Smem>
+__device__ __forceinline__ bool gather(const ScanArgs& a, const Tile& t, const Place<V>& p, int warp, int f, Smem& sm) {
+  constexpr int kEach = kGroup / kWarps;
+  const int c0 = warp * kEach;
+  uint64_t w[kEach][V];
+  uint32_t g[V];
+  const bool state = warp == 0 && p.first > 0;
+  const bool ok = wait_for(a, [&] {
+    if (!p.on) return true;
+#pragma unroll
+    for (int c = 0; c < kEach; ++c)
+      if (c0 + c < p.n) peek(p.map - (int64_t)(p.n - c0 - c) * a.D, w[c]);
+    if (state) peek(p.group, g);
+    bool there = true;
+#pragma unroll
+    for (int c = 0; c < kEach; ++c)
+      if (c0 + c < p.n)
+#pragma unroll
+        for (int i = 0; i < V; ++i) there &= w[c][i] != kNoMap;
+    if (state)
+#pragma unroll
+      for (int i = 0; i < V; ++i) there &= g[i] != kNoState;
+    return there;
+  });
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float A = 1.f, h = 0.f;
+    if (p.on)
+#pragma unroll
+      for (int c = 0; c < kEach; ++c)
+        if (c0 + c < p.n) {
+          const float ca = __uint_as_float((uint32_t)w[c][i]);
+          h = decay_fma(ca, h, __uint_as_float((uint32_t)(w[c][i] >> 32)));
+          A *= ca;
+        }
+    sm.pre[warp][f + i] = make_float2(A, h);
+    if (warp == 0) {
+      float e = 0.f;
+      if (p.on) e = state ? __uint_as_float(g[i]) : a.enter0 ? a.enter0[t.b * a.enter0_stride + p.d + i] : 0.f;
+      sm.enter[f + i] = e;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) h[i] = 0.f;
-  if (first) {
-    uint32_t w[V];
-    if (!wait_for(a, [&] {
-          if (!on) return true;
-          peek(group, w);
-          bool there = true;
-#pragma unroll
-          for (int i = 0; i < V; ++i) there &= w[i] != kNoState;
-          return there;
-        }))
-      return false;
-    if (on)
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = __uint_as_float(w[i]);
-  } else if (on && a.enter0) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = a.enter0[t.b * a.enter0_stride + d + i];
-  }
-  // loads five ahead of their folds (all fifteen would spill)
-#pragma unroll
-  for (int c0 = 0; c0 < kGroup - 1; c0 += 5) {
-    if (c0 >= n) break;
-    uint64_t w[5][V];
-    if (!wait_for(a, [&] {
-          if (!on) return true;
-#pragma unroll
-          for (int c = 0; c < 5; ++c)
-            if (c0 + c < n) peek(map - (int64_t)(n - c0 - c) * a.D, w[c]);
-          bool there = true;
-#pragma unroll
-          for (int c = 0; c < 5; ++c)
-            if (c0 + c < n)
-#pragma unroll
-              for (int i = 0; i < V; ++i) there &= w[c][i] != kNoMap;
-          return there;
-        }))
-      return false;
-    if (on)
-#pragma unroll
-      for (int c = 0; c < 5; ++c)
-        if (c0 + c < n)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            h[i] = decay_fma(__uint_as_float((uint32_t)w[c][i]), h[i], __uint_as_float((uint32_t)(w[c][i] >> 32)));
-  }
-  if (on && n == kGroup - 1 && !last) {
+  return ok;
+}
+
+// The state leaving the chunk, for the next group and the caller.
+template <int V>
+__device__ __forceinline__ void pass_on(const ScanArgs& a, const Tile& t, const Place<V>& p, const float (&A)[V],
+                                        const float (&m)[V], const float (&h)[V]) {
+  if (!p.on) return;
+  if (p.n == kGroup - 1 && !p.last) {
     uint32_t w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) w[i] = not_ones(decay_fma(A[i], h[i], m[i]));
-    publish(group + a.D, w);
+    publish(p.group + a.D, w);
   }
-  if (on && last && a.leave) {
+  if (p.last && a.leave) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) a.leave[(int64_t)t.b * a.D + d + i] = decay_fma(A[i], h[i], m[i]);
+    for (int i = 0; i < V; ++i) a.leave[(int64_t)t.b * a.D + p.d + i] = decay_fma(A[i], h[i], m[i]);
   }
-  return true;
 }
-
-template <typename T>
-struct ScanSmem {
-  float2 map[kWarps][kFT<T>];    // (A, h) of every warp's span
-  float2 back[kWarps][kFT<T>];   // backward: the same of the reverse recurrence
-  float enter[kFT<T>], enter_back[kFT<T>];
-  uint64_t bar;
-  int abort_flag, unit, ok;
-};
 
 // Which tile this block takes: drawn from the counter, or (one chunk: nothing
 // to wait for) the block's own index.
@@ -370,11 +392,22 @@ __device__ __forceinline__ bool span_map_of(const uint8_t* pg, const uint8_t* px
 template <typename T, bool kShut>
 __device__ __forceinline__ void span_out(const uint8_t* pg, uint8_t* px, uint32_t starts, typename Lane<T>::Val h) {
   using X = Lane<T>;
-#pragma unroll 8
-  for (int s = 0; s < kSpan; ++s) {
-    const typename X::Val g = gate_at<T, kShut>(read4<T>(pg + s * kRowBytes), starts, s);
-    h = step<T, kShut>(g, h, X::open(read4<T>(px + s * kRowBytes)));
-    write4<T>(px + s * kRowBytes, X::shut(h));
+  // (reads of eight tokens ahead of their writes, which might alias for all the compiler knows)
+#pragma unroll
+  for (int s0 = 0; s0 < kSpan; s0 += 8) {
+    typename X::Raw g[8], x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      g[i] = read4<T>(pg + (s0 + i) * kRowBytes);
+      x[i] = read4<T>(px + (s0 + i) * kRowBytes);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h = step<T, kShut>(gate_at<T, kShut>(g[i], starts, s0 + i), h, X::open(x[i]));
+      x[i] = X::shut(h);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) write4<T>(px + (s0 + i) * kRowBytes, x[i]);
   }
 }
 
@@ -397,14 +430,27 @@ __device__ __forceinline__ void span_back(uint8_t* pg, uint8_t* pd, uint32_t sta
                                           const typename Lane<T>::Val (&before)[kSpan]) {
   using X = Lane<T>;
 #pragma unroll
-  for (int s = kSpan - 1; s >= 0; --s) {
-    const typename X::Val g = gate_at<T, kShut>(read4<T>(pg + s * kRowBytes), starts, s);
-    const typename X::Val dh = X::add(X::open(read4<T>(pd + s * kRowBytes)), e);
-    e = times<T, kShut>(g, dh);
-    // (where the gate is zero e is, and before may not be finite)
-    const typename X::Val dg = times<T, kShut>(e, before[s]);
-    write4<T>(pd + s * kRowBytes, X::shut(dh));
-    write4<T>(pg + s * kRowBytes, X::shut(dg));
+  for (int s0 = kSpan - 8; s0 >= 0; s0 -= 8) {
+    typename X::Raw g[8], dy[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      g[i] = read4<T>(pg + (s0 + i) * kRowBytes);
+      dy[i] = read4<T>(pd + (s0 + i) * kRowBytes);
+    }
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const typename X::Val a = gate_at<T, kShut>(g[i], starts, s0 + i);
+      const typename X::Val dh = X::add(X::open(dy[i]), e);
+      e = times<T, kShut>(a, dh);
+      dy[i] = X::shut(dh);
+      // (where the gate is zero e is, and before may not be finite)
+      g[i] = X::shut(times<T, kShut>(e, before[s0 + i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      write4<T>(pd + (s0 + i) * kRowBytes, dy[i]);
+      write4<T>(pg + (s0 + i) * kRowBytes, g[i]);
+    }
   }
 }
 
@@ -429,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 6) scan_kernel(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tx = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   uint8_t* tg = tx + kTileBytes;
-  __shared__ ScanSmem<T> sm;
+  __shared__ ScanSmem<T, false> sm;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sm.abort_flag = 0;
@@ -463,26 +509,26 @@ __global__ void __launch_bounds__(kThreads, 6) scan_kernel(const __grid_constant
     for (int i = 0; i < V; ++i) sm.map[warp][f + i] = make_float2(A[i], h[i]);
   }
   __syncthreads();
+  const Place<V> pl = place_of<V>(a, t, (int64_t)t.tile * F + f);
+  float cA[V], cm[V];   // warp 0: the chunk's map
   if (warp == 0) {
-    float A[V], m[V], h[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 1.f, m[i] = 0.f;
-    fold<V, F>(sm.map, f, 0, kWarps, 1, A, m);
-    const int64_t d = (int64_t)t.tile * F + f;
-    const bool ok = hand_off<V>(a, t, d, d < a.D, A, m, h);
-    if (ok && a.chunk_state && d < a.D) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) a.chunk_state[((int64_t)t.b * a.C + t.c) * a.D + d + i] = h[i];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) sm.enter[f + i] = h[i];
-    if (lane == 0) sm.ok = ok;
+    for (int i = 0; i < V; ++i) cA[i] = 1.f, cm[i] = 0.f;
+    fold<V, F>(sm.map, f, 0, kWarps, 1, cA, cm);
+    publish_map(pl, cA, cm);
   }
-  __syncthreads();
-  if (!sm.ok) return;
+  if (__syncthreads_or(!gather(a, t, pl, warp, f, sm))) return;
   float A[V], h[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = sm.enter[f + i], A[i] = 1.f;
+  fold<V, F>(sm.pre, f, 0, kWarps, 1, A, h);
+  if (warp == 0) {
+    pass_on(a, t, pl, cA, cm, h);
+    if (a.chunk_state && pl.on) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) a.chunk_state[((int64_t)t.b * a.C + t.c) * a.D + pl.d + i] = h[i];
+    }
+  }
   fold<V, F>(sm.map, f, 0, warp, 1, A, h);
   if (shut) span_out<T, true>(pg, px, starts, X::put(h));
   else span_out<T, false>(pg, px, starts, X::put(h));
@@ -558,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tx = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   uint8_t *tg = tx + kTileBytes, *td = tg + kTileBytes;
-  __shared__ ScanSmem<T> sm;
+  __shared__ ScanSmem<T, true> sm;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sm.abort_flag = 0;
@@ -603,17 +649,15 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_cons
     }
   }
   __syncthreads();
+  const Place<V> pl = place_of<V>(a, t, d);
+  float cA[V], cm[V];   // warp 0: the chunk's map
   if (warp == 0) {
-    float A[V], m[V], e[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 1.f, m[i] = 0.f;
-    fold<V, F>(sm.back, f, kWarps - 1, -1, -1, A, m);
-    const bool ok = hand_off<V>(a, t, d, d < a.D, A, m, e);
-#pragma unroll
-    for (int i = 0; i < V; ++i) sm.enter_back[f + i] = e[i];
-    if (lane == 0) sm.ok = ok;
+    for (int i = 0; i < V; ++i) cA[i] = 1.f, cm[i] = 0.f;
+    fold<V, F>(sm.back, f, kWarps - 1, -1, -1, cA, cm);
+    publish_map(pl, cA, cm);
   }
-  // meanwhile: the states of this span
+  // the states of this span, while the maps of others arrive
   float A[V], h[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = h0[i], A[i] = 1.f;
@@ -621,11 +665,12 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_cons
   typename X::Val before[kSpan];
   if (shut) span_states<T, true>(pg, px, starts, X::put(h), before);
   else span_states<T, false>(pg, px, starts, X::put(h), before);
-  __syncthreads();
-  if (!sm.ok) return;
+  if (__syncthreads_or(!gather(a, t, pl, warp, f, sm))) return;
   float e[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) e[i] = sm.enter_back[f + i];
+  for (int i = 0; i < V; ++i) e[i] = sm.enter[f + i];
+  fold<V, F>(sm.pre, f, 0, kWarps, 1, A, e);
+  if (warp == 0) pass_on(a, t, pl, cA, cm, e);
   fold<V, F>(sm.back, f, kWarps - 1, warp, -1, A, e);
   if (shut) span_back<T, true>(pg, pd, starts, X::put(e), before);
   else span_back<T, false>(pg, pd, starts, X::put(e), before);
