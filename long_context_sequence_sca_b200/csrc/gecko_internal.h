@@ -260,7 +260,7 @@ struct QkProblem {
   double rate[kMaxRotPairs];
 };
 
-size_t qk_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d, int dtype);   // backward
+size_t qk_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d);   // backward
 cudaError_t launch_qk(const QkProblem& p, cudaStream_t st);
 cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
 

@@ -156,7 +156,7 @@ int qk_backward(const void* z, const float* scale, const int64_t* pos, const voi
   int rc;
   if ((rc = check_qk_sizes(B, T, H, d, eps, rot_dim, rot_base, dtype))) return rc;
   if ((rc = check_pointers({z, scale, dq, dk, dqm, dkm, dz, dscale, dshift}, {pos}))) return rc;
-  if ((rc = check_workspace(ws, ws_bytes, qk_workspace_bytes(B, T, H, d, dtype)))) return rc;
+  if ((rc = check_workspace(ws, ws_bytes, qk_workspace_bytes(B, T, H, d)))) return rc;
   QkProblem p{};
   p.z = z, p.scale = scale, p.pos = pos;
   p.dout[0] = dq, p.dout[1] = dk, p.dout[2] = dqm, p.dout[3] = dkm;
@@ -270,7 +270,7 @@ extern "C" int gecko_qk_workspace(int64_t B, int64_t T, int64_t H, int64_t d, in
   return guarded([&] {
     if (!bytes) return fail(GECKO_ERR_ARG, "bytes is NULL");
     if (int rc = check_qk_sizes(B, T, H, d, 1.f, 0, 1.0, dtype)) return rc;
-    *bytes = (int64_t)qk_workspace_bytes(B, T, H, d, dtype);
+    *bytes = (int64_t)qk_workspace_bytes(B, T, H, d);
     return GECKO_OK;
   });
 }

@@ -14,11 +14,12 @@
 namespace gecko {
 namespace {
 
-constexpr int kFwdThreads = 256, kBwdThreads = 128;
-// Resident blocks per SM, by the registers of their prefetched rows.
-constexpr int kFwdBlocks = 2;
-constexpr int bwd_blocks(size_t elem) { return elem == 2 ? 3 : 2; }
-constexpr int kQkTokens = 32;                          // tokens per fill of the sine table
+constexpr int kFwdThreads = 256, kFwdBlocks = 2;     // threads per block, blocks per SM (registers)
+constexpr int kBwdThreads = 384, kBwdBlocks = 1;
+// Rounds of rows on their way to shared memory in the backward (five rows of 16
+// or 32 bytes per thread each).
+template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 3;
+constexpr int kQkTokens = 48;   // tokens per fill of the sine table, at least a round's
 enum { kRotNone = 0, kRotHalves = 1, kRotInterleaved = 2 };
 
 struct QkArgs {
@@ -38,8 +39,13 @@ struct QkArgs {
   double rate[kMaxRotPairs];
 };
 
-struct F8 {
-  float v[8];
+// 8 features as four packed fp32 pairs.
+struct P4 {
+  uint64_t v[4];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack2(0.f, 0.f);
+  }
 };
 
 // 8 elements as loaded, so that a prefetched row takes as few registers as it can.
@@ -51,107 +57,127 @@ template <> struct Raw8<float> {
     b = *reinterpret_cast<const float4*>(p + 4);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ F8 get() const { return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+  __device__ __forceinline__ P4 get() const {
+    return {{pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w)}};
+  }
 };
 template <> struct Raw8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ F8 get() const {
-    F8 r;
+  __device__ __forceinline__ P4 get() const {
+    P4 r;
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.v[2 * i] = __uint_as_float(w[i] << 16);
-      r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      r.v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     return r;
   }
 };
-__device__ __forceinline__ F8 load8(const float* p) {
+__device__ __forceinline__ P4 load8(const float* p) {
   Raw8<float> r;
   r.load(p);
   return r.get();
 }
-__device__ __forceinline__ void store8(float* p, const F8& f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+__device__ __forceinline__ void store8(float* p, const P4& f) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(f.v[i], v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& f) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f.v[0], f.v[1]), pack_bf16x2(f.v[2], f.v[3]),
-                                            pack_bf16x2(f.v[4], f.v[5]), pack_bf16x2(f.v[6], f.v[7]));
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const P4& f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(f.v[i], lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float dot8(const P4& a, const P4& b) {
+  const uint64_t s = ffma2(a.v[2], b.v[2], fmul2(a.v[0], b.v[0])), t = ffma2(a.v[3], b.v[3], fmul2(a.v[1], b.v[1]));
+  float lo, hi;
+  unpack2(fadd2(s, t), lo, hi);
+  return lo + hi;
 }
 
-// The sine table: (cos, sin) of every rotated pair of the fill's tokens.  A lane
-// reads kPer pairs of a row, 16 bytes (two pairs) at a time; the 16-byte pieces
-// of a row are ordered so that the lanes of one read are consecutive.
+// The sine table: (cos, cos, sin, sin) of every two neighbouring rotated pairs
+// of the fill's tokens.  A lane reads kPer pairs of a row, two with each
+// access; these pieces of a row are ordered so that the lanes of one access
+// are consecutive.
 template <int kRot>
 constexpr int kPer = kRot == kRotInterleaved ? 4 : 8;
 
-template <int kRot>
-__device__ __forceinline__ int turn_slot(int pair, int pairs) {
-  constexpr int kPieces = kPer<kRot> / 2;   // pieces per lane
-  const int piece = pair >> 1;
-  return ((piece % kPieces) * (pairs / kPer<kRot>) + piece / kPieces) * 2 + (pair & 1);
-}
-
 template <int kRot, int kThreads>
-__device__ __forceinline__ void fill_turns(float2* turns, const double* rate, const QkArgs& a, int64_t n0, int n,
+__device__ __forceinline__ void fill_turns(float4* turns, const double* rate, const QkArgs& a, int64_t n0, int n,
                                            uint32_t t0) {
-  const int pairs = a.rot_dim / 2;
+  constexpr int kPieces = kPer<kRot> / 2;   // pieces per lane
+  const int pairs = a.rot_dim / 2, readers = pairs / kPer<kRot>;
+  float* out = reinterpret_cast<float*>(turns);
   for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-    const int k = i / pairs, pair = i - k * pairs;
+    const int k = i / pairs, pair = i - k * pairs, piece = pair >> 1;
     const int64_t pos = a.pos ? a.pos[n0 + k] : a.pos0 + (t0 + k) % (uint32_t)a.T;
     const double rev = (double)pos * rate[pair];
     float s, c;
     sincospif((float)(2.0 * (rev - rint(rev))), &s, &c);
-    turns[k * pairs + turn_slot<kRot>(pair, pairs)] = make_float2(c, s);
+    const int at = 4 * (k * (pairs / 2) + piece % kPieces * readers + piece / kPieces) + (pair & 1);
+    out[at] = c;
+    out[at + 2] = s;
   }
 }
 
-struct Turn8 {
-  float2 cs[8];
+// What turns this lane's 8 features: p -> p c + partner s, as packed pairs; the
+// partner is the other half's feature (halves), or the other of the two
+// (interleaved).  A lane beyond the rotated features gets c = 1, s = 0.
+struct Turn {
+  uint64_t c[4], s[4];
 };
 
-// This lane's (cos, sin) of one row: of its pairs (interleaved), or of the
-// pairs that its 8 features belong to (halves; the two halves share them).
 template <int kRot>
-__device__ __forceinline__ void load_turn(Turn8& r, const float2* row, int l, int rot_dim) {
-  const int lanes = rot_dim / 16;   // halves: lanes per half
+__device__ __forceinline__ void load_turn(Turn& r, const float4* row, int l, int rot_dim, float sign) {
+  constexpr int kPieces = kPer<kRot> / 2;
   const int readers = rot_dim / 2 / kPer<kRot>;
-  const int at = kRot == kRotHalves && l >= lanes ? l - lanes : l;
+  const bool in = 8 * l < rot_dim;
+  if (kRot == kRotHalves) {
+    const bool upper = l >= readers;
+    const float sg = upper ? sign : -sign;
+    const float4* p = row + (in ? upper ? l - readers : l : 0);
 #pragma unroll
-  for (int i = 0; i < kPer<kRot> / 2; ++i) {
-    const float4 v = *reinterpret_cast<const float4*>(row + (i * readers + (at < readers ? at : 0)) * 2);
-    r.cs[2 * i] = make_float2(v.x, v.y);
-    r.cs[2 * i + 1] = make_float2(v.z, v.w);
+    for (int i = 0; i < kPieces; ++i) {
+      const float4 v = p[i * readers];
+      r.c[i] = in ? pack2(v.x, v.y) : pack2(1.f, 1.f);
+      r.s[i] = in ? pack2(v.z * sg, v.w * sg) : pack2(0.f, 0.f);
+    }
+  } else {
+    const float4* p = row + (in ? l : 0);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const float4 v = p[i * readers];
+      const float s0 = v.z * sign, s1 = v.w * sign;
+      r.c[2 * i] = in ? pack2(v.x, v.x) : pack2(1.f, 1.f);
+      r.c[2 * i + 1] = in ? pack2(v.y, v.y) : pack2(1.f, 1.f);
+      r.s[2 * i] = in ? pack2(-s0, s0) : pack2(0.f, 0.f);
+      r.s[2 * i + 1] = in ? pack2(-s1, s1) : pack2(0.f, 0.f);
+    }
   }
 }
 
-// The 8 features 8 l .. 8 l + 7 of a row turned (sign -1: turned back).  src: the
-// lane that holds the other half of this lane's pairs (halves), which every
-// lane of the warp must pass here.
+// src: the lane that holds the partners (halves), which every lane of the
+// warp must pass here.
 template <int kRot>
-__device__ __forceinline__ void turn8(F8& p, const Turn8& r, int l, int rot_dim, int src, float sign) {
-  if (kRot == kRotInterleaved) {
-    if (8 * l < rot_dim) {
+__device__ __forceinline__ void turn8(P4& p, const Turn& r, int src) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = p.v[2 * i], b = p.v[2 * i + 1], s = sign * r.cs[i].y;
-        p.v[2 * i] = a * r.cs[i].x - b * s;
-        p.v[2 * i + 1] = b * r.cs[i].x + a * s;
-      }
-    }
-  } else if (kRot == kRotHalves) {
-    const int half = rot_dim / 16;   // lanes per half
-    const float sg = l >= half ? sign : -sign;
-    const bool in = l < 2 * half;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, p.v[i], src);
-      const float t = p.v[i] * r.cs[i].x + sg * r.cs[i].y * o;
-      if (in) p.v[i] = t;
-    }
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(p.v[i], lo, hi);
+    uint64_t partner;
+    if (kRot == kRotHalves)
+      partner = pack2(__shfl_sync(0xffffffffu, lo, src), __shfl_sync(0xffffffffu, hi, src));
+    else
+      partner = pack2(hi, lo);
+    p.v[i] = ffma2(partner, r.s[i], fmul2(p.v[i], r.c[i]));
   }
 }
 
@@ -204,13 +230,13 @@ struct Walk {
 
 template <typename T, int D, int kRot>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks) qk_kernel(const __grid_constant__ QkArgs a) {
-  __shared__ __align__(16) float2 turns[kRot == kRotNone ? 1 : kQkTokens * D / 2];
+  __shared__ float4 turns[kRot == kRotNone ? 1 : kQkTokens * D / 4];
   __shared__ double rate[kMaxRotPairs];   // the parameter bank would serialise the lanes' reads
   if (kRot != kRotNone && threadIdx.x < a.rot_dim / 2) rate[threadIdx.x] = a.rate[threadIdx.x];
   const int64_t first = (int64_t)blockIdx.x * a.tokens_per_block;
   const int64_t last = min(first + a.tokens_per_block, a.n_tokens);
   const Slot s = my_slot<D>(a);
-  F8 sc[4], sh[4];
+  P4 sc[4], sh[4];
   if (s.on) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -233,131 +259,180 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks) qk_kernel(const __gri
   w = w0;
   w.step(s.tsub, a.T);
   // every lane of a warp makes the same number of rounds (shuffles)
-  for (int k0 = 0, fill = 0; k0 < len; k0 += a.token_slots) {
+  for (int k0 = 0, fill = 0, fill0 = 0; k0 < len; k0 += a.token_slots) {
     if (kRot != kRotNone && k0 == fill) {
       const int n = min(a.tokens_per_fill, len - k0);
       __syncthreads();
       fill_turns<kRot, kFwdThreads>(turns, rate, a, first + k0, n, w0.t);
       w0.step(n, a.T);
+      fill0 = fill;   // the table's first token; the next fill's
       fill += n;
       __syncthreads();
     }
     const int k = k0 + s.tsub;
     const bool on = s.on && k < len;
-    F8 z = z0.get();
+    P4 z = z0.get();
     z0 = z1;
     if (s.on && k + 2 * a.token_slots < len) z1.load(zp + (k + 2 * a.token_slots) * zrow);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(z.v[i], z.v[i], ss);
-    const float nrm = sqrtf(row_sum<D>(ss));
+    const float nrm = sqrtf(row_sum<D>(dot8(z, z)));
     const float inv = 1.f / (nrm < a.eps ? a.eps : nrm);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z.v[i] *= inv;
-    Turn8 turn;
+    for (int i = 0; i < 4; ++i) z.v[i] = fmul2(z.v[i], pack2(inv, inv));
+    Turn turn;
     if (kRot != kRotNone)
-      load_turn<kRot>(turn, turns + (on ? k % a.tokens_per_fill : 0) * (a.rot_dim / 2), s.l, a.rot_dim);
+      load_turn<kRot>(turn, turns + (on ? k - fill0 : 0) * (a.rot_dim / 4), s.l, a.rot_dim, 1.f);
     const int64_t at = w.row(a.H, a.T, s.head) * D + 8 * s.l;
     w.step(a.token_slots, a.T);
 #pragma unroll
     for (int o = 0; o < 4; ++o) {
-      F8 p;
+      P4 p;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p.v[i] = fmaf(sc[o].v[i], z.v[i], sh[o].v[i]);
-      if (kRot != kRotNone && o < 2) turn8<kRot>(p, turn, s.l, a.rot_dim, s.src, 1.f);
+      for (int i = 0; i < 4; ++i) p.v[i] = ffma2(sc[o].v[i], z.v[i], sh[o].v[i]);
+      if (kRot != kRotNone && o < 2) turn8<kRot>(p, turn, s.src);
       if (on) store8(static_cast<T*>(a.out[o]) + at, p);
     }
   }
 }
 
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+
+// Each thread has its rows' pieces (z and the four output gradients) brought
+// into its own slots of a ring in shared memory, kStages rounds ahead.  (In
+// registers one round ahead was all there was room for beside the 64 running
+// sums: 49 us at 2 x 5003 x 16 x 64 against 33 us.)
 template <typename T, int D, int kRot>
-__global__ void __launch_bounds__(kBwdThreads, bwd_blocks(sizeof(T))) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
-  __shared__ __align__(16) float2 turns[kRot == kRotNone ? 1 : kQkTokens * D / 2];
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int S = kStages<T>, kParts = sizeof(T) / 2;   // 16-byte parts of a thread's 8 elements
+  extern __shared__ uint4 smem[];
+  uint4* ring = smem;                                          // [S][5][kParts][threads]
+  float4* turns = reinterpret_cast<float4*>(smem + S * 5 * kParts * kBwdThreads);
   __shared__ double rate[kMaxRotPairs];
   if (kRot != kRotNone && threadIdx.x < a.rot_dim / 2) rate[threadIdx.x] = a.rate[threadIdx.x];
   const int64_t first = (int64_t)blockIdx.x * a.tokens_per_block;
   const int64_t last = min(first + a.tokens_per_block, a.n_tokens);
   const Slot s = my_slot<D>(a);
-  F8 sc[4], ds[4] = {}, df[4] = {};
+  P4 sc[4], ds[4], df[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ds[i].zero(), df[i].zero(), sc[i].zero();
   if (s.on) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = load8(a.scale + ((int64_t)i * a.H + s.head) * D + 8 * s.l);
   }
   const int len = (int)(last - first);
-  const int64_t zrow = (int64_t)a.H * D, z_at = (first * a.H + s.head) * D + 8 * s.l;
+  const int64_t zrow = (int64_t)a.H * D, z_at = (first * a.H + (s.on ? s.head : 0)) * D + 8 * s.l;
   Walk w, w0;
   w0.start(first, a.T);
   w = w0;
   w.step(s.tsub, a.T);
-  // this round's z and output gradients; the next round's are loaded before
-  // these are worked on
-  Raw8<T> raw[5];
-  auto fetch = [&](int k) {
-    if (s.on && k < len) {
-      const int64_t at = w.row(a.H, a.T, s.head) * D + 8 * s.l;
-      raw[4].load(static_cast<const T*>(a.z) + z_at + k * zrow);
+  auto fetch = [&](int k, int stage) {   // in order of k
+    uint4* to = ring + stage * 5 * kParts * kBwdThreads + threadIdx.x;
+    const bool on = s.on && k < len;
+    const int64_t at = on ? w.row(a.H, a.T, s.head) * D + 8 * s.l : 0, z = on ? z_at + k * zrow : 0;
 #pragma unroll
-      for (int o = 0; o < 4; ++o) raw[o].load(static_cast<const T*>(a.dout[o]) + at);
-    } else {
+    for (int h = 0; h < kParts; ++h) {
+      constexpr int kStep = 16 / sizeof(T);
 #pragma unroll
-      for (int o = 0; o < 5; ++o) raw[o].zero();
+      for (int o = 0; o < 4; ++o)
+        copy16(to + (o * kParts + h) * kBwdThreads, static_cast<const T*>(a.dout[o]) + at + h * kStep, on);
+      copy16(to + (4 * kParts + h) * kBwdThreads, static_cast<const T*>(a.z) + z + h * kStep, on);
     }
+    cp_async_commit();
     w.step(a.token_slots, a.T);
   };
-  fetch(s.tsub);
-  for (int k0 = 0, fill = 0; k0 < len; k0 += a.token_slots) {
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(s.tsub + i * a.token_slots, i);
+  int stage = 0;
+  for (int k0 = 0, fill = 0, fill0 = 0; k0 < len; k0 += a.token_slots) {
     if (kRot != kRotNone && k0 == fill) {
       const int n = min(a.tokens_per_fill, len - k0);
       __syncthreads();
       fill_turns<kRot, kBwdThreads>(turns, rate, a, first + k0, n, w0.t);
       w0.step(n, a.T);
+      fill0 = fill;   // the table's first token; the next fill's
       fill += n;
       __syncthreads();
     }
     const int k = k0 + s.tsub;
     const bool on = s.on && k < len;
-    F8 z = raw[4].get(), g = {}, p[4];
+    // the stage that the round before was read from is free again (only this thread reads it)
+    fetch(k + (S - 1) * a.token_slots, stage == 0 ? S - 1 : stage - 1);
+    cp_async_wait<S - 1>();
+    P4 z, g, p[4];
+    {
+      const uint4* from = ring + stage * 5 * kParts * kBwdThreads + threadIdx.x;
+      Raw8<T> raw;
 #pragma unroll
-    for (int o = 0; o < 4; ++o) p[o] = raw[o].get();
-    fetch(k + a.token_slots);
-    float ss = 0.f;
+      for (int o = 0; o < 5; ++o) {
+        uint4* to = reinterpret_cast<uint4*>(&raw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(z.v[i], z.v[i], ss);
-    const float nrm = sqrtf(row_sum<D>(ss));
+        for (int h = 0; h < kParts; ++h) to[h] = from[(o * kParts + h) * kBwdThreads];
+        if (o < 4) p[o] = raw.get();
+        else z = raw.get();
+      }
+    }
+    if (++stage == S) stage = 0;
+    g.zero();
+    const float nrm = sqrtf(row_sum<D>(dot8(z, z)));
     const float inv = 1.f / (nrm < a.eps ? a.eps : nrm);
+    const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z.v[i] *= inv;
+    for (int i = 0; i < 4; ++i) z.v[i] = fmul2(z.v[i], inv2);
     if (kRot != kRotNone) {
-      Turn8 turn;
-      load_turn<kRot>(turn, turns + (on ? k % a.tokens_per_fill : 0) * (a.rot_dim / 2), s.l, a.rot_dim);
-      turn8<kRot>(p[0], turn, s.l, a.rot_dim, s.src, -1.f);
-      turn8<kRot>(p[1], turn, s.l, a.rot_dim, s.src, -1.f);
+      Turn turn;
+      load_turn<kRot>(turn, turns + (on ? k - fill0 : 0) * (a.rot_dim / 4), s.l, a.rot_dim, -1.f);
+      turn8<kRot>(p[0], turn, s.src);
+      turn8<kRot>(p[1], turn, s.src);
     }
     // a row that is off is all zeros and adds nothing
 #pragma unroll
     for (int o = 0; o < 4; ++o)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g.v[i] = fmaf(sc[o].v[i], p[o].v[i], g.v[i]);
-        ds[o].v[i] = fmaf(p[o].v[i], z.v[i], ds[o].v[i]);
-        df[o].v[i] += p[o].v[i];
+      for (int i = 0; i < 4; ++i) {
+        g.v[i] = ffma2(sc[o].v[i], p[o].v[i], g.v[i]);
+        ds[o].v[i] = ffma2(p[o].v[i], z.v[i], ds[o].v[i]);
+        df[o].v[i] = fadd2(df[o].v[i], p[o].v[i]);
       }
-    float zg = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) zg = fmaf(z.v[i], g.v[i], zg);
-    zg = row_sum<D>(zg);
+    float zg = row_sum<D>(dot8(z, g));
     if (nrm <= a.eps) zg = 0.f;   // z' = z / eps there: no term through the norm
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g.v[i] = (g.v[i] - z.v[i] * zg) * inv;
+    for (int i = 0; i < 4; ++i) g.v[i] = fmul2(ffma2(z.v[i], pack2(-zg, -zg), g.v[i]), inv2);
     if (on) store8(static_cast<T*>(a.dz) + z_at + k * zrow, g);
   }
-  if (s.on) {
-    const int64_t hd = (int64_t)a.H * D;
-    float* out = a.part + ((int64_t)blockIdx.x * a.token_slots + s.tsub) * 8 * hd + (int64_t)s.head * D + 8 * s.l;
+  cp_async_wait<0>();
+  // The token slots' sums into the first slot's, in order, through the ring.
+  const int row_threads = a.heads_per_block * (D / 8), me = threadIdx.x % row_threads;
+  ulonglong2* box = reinterpret_cast<ulonglong2*>(smem);   // [16][row_threads]
+  for (int t = 1; t < a.token_slots; ++t) {
+    __syncthreads();
+    if (s.tsub == t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const P4& v = i < 4 ? ds[i] : df[i - 4];
+        box[(2 * i) * row_threads + me] = make_ulonglong2(v.v[0], v.v[1]);
+        box[(2 * i + 1) * row_threads + me] = make_ulonglong2(v.v[2], v.v[3]);
+      }
+    __syncthreads();
+    if (s.tsub == 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        P4& v = i < 4 ? ds[i] : df[i - 4];
+        const ulonglong2 lo = box[(2 * i) * row_threads + me], hi = box[(2 * i + 1) * row_threads + me];
+        v.v[0] = fadd2(v.v[0], lo.x);
+        v.v[1] = fadd2(v.v[1], lo.y);
+        v.v[2] = fadd2(v.v[2], hi.x);
+        v.v[3] = fadd2(v.v[3], hi.y);
+      }
+  }
+  if (s.on && s.tsub == 0) {
+    float* out = a.part + (int64_t)blockIdx.x * 8 * zrow + (int64_t)s.head * D + 8 * s.l;
 #pragma unroll
     for (int o = 0; o < 4; ++o) {
-      store8(out + o * hd, ds[o]);
-      store8(out + (4 + o) * hd, df[o]);
+      store8(out + o * zrow, ds[o]);
+      store8(out + (4 + o) * zrow, df[o]);
     }
   }
 }
@@ -386,14 +461,23 @@ struct Plan {
   int64_t tokens_per_block, token_blocks;
 };
 
-// Heads are split over blocks so that a block's row slots hold whole heads, the
-// tokens evenly over one wave of blocks.
+// Heads are split over blocks so that a block's row slots hold whole heads, one
+// token's or several tokens', and as few slots as possible stay empty; the tokens
+// evenly over one wave of blocks.
 Plan plan_of(int64_t n_tokens, int64_t H, int64_t d, int threads, int blocks_per_sm) {
   const int64_t slots = threads / (d / 8);
   Plan pl;
-  pl.head_blocks = (int)((H + slots - 1) / slots);
-  pl.heads_per_block = (int)((H + pl.head_blocks - 1) / pl.head_blocks);
-  pl.token_slots = (int)(slots / pl.heads_per_block);
+  double best = 0.0;
+  for (int64_t n = (H + slots - 1) / slots; n <= H; ++n) {
+    const int64_t heads = (H + n - 1) / n, tokens = slots / heads;
+    const double used = (double)H * tokens / (double)(n * slots);
+    if (used > best + 0.05) {   // more blocks fill the sine table more often
+      best = used;
+      pl.head_blocks = (int)((H + heads - 1) / heads);
+      pl.heads_per_block = (int)heads;
+      pl.token_slots = (int)tokens;
+    }
+  }
   int64_t blocks = (int64_t)blocks_per_sm * sm_count() / pl.head_blocks;
   if (blocks < 1) blocks = 1;
   const int64_t most = int64_t(1) << 30;   // tokens of a block are counted in 32 bits
@@ -431,7 +515,7 @@ QkArgs args_of(const QkProblem& p, const Plan& pl) {
 }
 
 template <typename T, int D>
-void run(const QkProblem& p, const Plan& pl, bool backward, cudaStream_t st) {
+cudaError_t run(const QkProblem& p, const Plan& pl, bool backward, cudaStream_t st) {
   const QkArgs a = args_of(p, pl);
   const dim3 grid((unsigned)pl.token_blocks, (unsigned)pl.head_blocks);
   const int rot = p.rot_dim == 0 ? kRotNone : p.interleaved ? kRotInterleaved : kRotHalves;
@@ -440,45 +524,40 @@ void run(const QkProblem& p, const Plan& pl, bool backward, cudaStream_t st) {
     else if (rot == kRotHalves) qk_kernel<T, D, kRotHalves><<<grid, kFwdThreads, 0, st>>>(a);
     else qk_kernel<T, D, kRotInterleaved><<<grid, kFwdThreads, 0, st>>>(a);
   } else {
-    if (rot == kRotNone) qk_bwd_kernel<T, D, kRotNone><<<grid, kBwdThreads, 0, st>>>(a);
-    else if (rot == kRotHalves) qk_bwd_kernel<T, D, kRotHalves><<<grid, kBwdThreads, 0, st>>>(a);
-    else qk_bwd_kernel<T, D, kRotInterleaved><<<grid, kBwdThreads, 0, st>>>(a);
+    const auto kern = rot == kRotNone     ? qk_bwd_kernel<T, D, kRotNone>
+                      : rot == kRotHalves ? qk_bwd_kernel<T, D, kRotHalves>
+                                          : qk_bwd_kernel<T, D, kRotInterleaved>;
+    const int smem = kStages<T> * 5 * (int)sizeof(T) / 2 * kBwdThreads * 16 + kQkTokens * D / 4 * 16;
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    kern<<<grid, kBwdThreads, smem, st>>>(a);
   }
-}
-
-void run(const QkProblem& p, const Plan& pl, bool backward, cudaStream_t st) {
-  if (p.dtype == kBF16) {
-    if (p.d == 128) run<__nv_bfloat16, 128>(p, pl, backward, st);
-    else run<__nv_bfloat16, 64>(p, pl, backward, st);
-  } else {
-    if (p.d == 128) run<float, 128>(p, pl, backward, st);
-    else run<float, 64>(p, pl, backward, st);
-  }
-}
-
-Plan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t d, int dtype) {
-  return plan_of(B * T, H, d, kBwdThreads, bwd_blocks(dtype == kBF16 ? 2 : 4));
-}
-
-}  // namespace
-
-size_t qk_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d, int dtype) {
-  const Plan pl = bwd_plan(B, T, H, d, dtype);
-  return sizeof(float) * (size_t)(pl.token_blocks * pl.token_slots) * 8 * H * d;
-}
-
-cudaError_t launch_qk(const QkProblem& p, cudaStream_t st) {
-  run(p, plan_of(p.B * p.T, p.H, p.d, kFwdThreads, kFwdBlocks), false, st);
   return cudaGetLastError();
 }
 
+cudaError_t run(const QkProblem& p, const Plan& pl, bool backward, cudaStream_t st) {
+  if (p.dtype == kBF16)
+    return p.d == 128 ? run<__nv_bfloat16, 128>(p, pl, backward, st) : run<__nv_bfloat16, 64>(p, pl, backward, st);
+  return p.d == 128 ? run<float, 128>(p, pl, backward, st) : run<float, 64>(p, pl, backward, st);
+}
+
+Plan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t d) { return plan_of(B * T, H, d, kBwdThreads, kBwdBlocks); }
+
+}  // namespace
+
+size_t qk_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d) {
+  return sizeof(float) * (size_t)bwd_plan(B, T, H, d).token_blocks * 8 * H * d;
+}
+
+cudaError_t launch_qk(const QkProblem& p, cudaStream_t st) {
+  return run(p, plan_of(p.B * p.T, p.H, p.d, kFwdThreads, kFwdBlocks), false, st);
+}
+
 cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st) {
-  const Plan pl = bwd_plan(p.B, p.T, p.H, p.d, p.dtype);
-  run(p, pl, true, st);
+  const Plan pl = bwd_plan(p.B, p.T, p.H, p.d);
+  if (cudaError_t e = run(p, pl, true, st)) return e;
   const int64_t cols = 4 * p.H * p.d;
-  qk_bwd_sum_kernel<<<(unsigned)(2 * cols / 32), 256, 0, st>>>(static_cast<const float*>(p.ws),
-                                                               (int)(pl.token_blocks * pl.token_slots), cols,
-                                                               p.dscale, p.dshift);
+  qk_bwd_sum_kernel<<<(unsigned)(2 * cols / 32), 256, 0, st>>>(static_cast<const float*>(p.ws), (int)pl.token_blocks,
+                                                               cols, p.dscale, p.dshift);
   return cudaGetLastError();
 }
 
