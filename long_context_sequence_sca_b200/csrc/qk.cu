@@ -115,51 +115,66 @@ __device__ __forceinline__ void fill_turns(float4* turns, const double* rate, co
                                            uint32_t t0) {
   constexpr int kPieces = kPer<kRot> / 2;   // pieces per lane
   const int pairs = a.rot_dim / 2, readers = pairs / kPer<kRot>;
-  float* out = reinterpret_cast<float*>(turns);
-  for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-    const int k = i / pairs, pair = i - k * pairs, piece = pair >> 1;
-    const int64_t pos = a.pos ? a.pos[n0 + k] : a.pos0 + (t0 + k) % (uint32_t)a.T;
-    const double rev = (double)pos * rate[pair];
+  // a thread keeps its pair and steps over tokens
+  const int step = kThreads / pairs, pair = threadIdx.x % pairs, piece = pair >> 1;
+  float* out = reinterpret_cast<float*>(turns) + 4 * (piece % kPieces * readers + piece / kPieces) + (pair & 1);
+  const double r = rate[pair];
+  if (threadIdx.x >= step * pairs) return;
+  for (int k = threadIdx.x / pairs; k < n; k += step) {
+    uint32_t t = t0 + k;
+    if (t >= a.T) t %= (uint32_t)a.T;
+    const int64_t pos = a.pos ? a.pos[n0 + k] : a.pos0 + t;
+    const double rev = (double)pos * r;
     float s, c;
     sincospif((float)(2.0 * (rev - rint(rev))), &s, &c);
-    const int at = 4 * (k * (pairs / 2) + piece % kPieces * readers + piece / kPieces) + (pair & 1);
-    out[at] = c;
-    out[at + 2] = s;
+    out[2 * k * pairs] = c;
+    out[2 * k * pairs + 2] = s;
   }
 }
 
 // What turns this lane's 8 features: p -> p c + partner s, as packed pairs; the
 // partner is the other half's feature (halves), or the other of the two
-// (interleaved).  A lane beyond the rotated features gets c = 1, s = 0.
+// (interleaved).
 struct Turn {
   uint64_t c[4], s[4];
 };
 
+// Where a lane reads its pieces: `at` + row and pieces `step` apart; a lane beyond
+// the rotated features reads an entry behind the table, c = 1 and s = 0.
+struct TurnPlace {
+  int at, row, step;
+  uint64_t sign;   // (halves) of the partner's term
+};
 template <int kRot>
-__device__ __forceinline__ void load_turn(Turn& r, const float4* row, int l, int rot_dim, float sign) {
-  constexpr int kPieces = kPer<kRot> / 2;
+__device__ __forceinline__ TurnPlace turn_place(float4* turns, int entries, int l, int rot_dim, float sign) {
   const int readers = rot_dim / 2 / kPer<kRot>;
-  const bool in = 8 * l < rot_dim;
+  const bool in = 8 * l < rot_dim, upper = kRot == kRotHalves && l >= readers;
+  if (threadIdx.x == 0) turns[entries] = make_float4(1.f, 1.f, 0.f, 0.f);
+  const float sg = upper ? sign : -sign;
+  return {in ? upper ? l - readers : l : entries, in ? rot_dim / 4 : 0, in ? readers : 0, pack2(sg, sg)};
+}
+
+template <int kRot>
+__device__ __forceinline__ void load_turn(Turn& r, const float4* turns, const TurnPlace& t, int k) {
+  const float4* p = turns + t.at + k * t.row;
   if (kRot == kRotHalves) {
-    const bool upper = l >= readers;
-    const float sg = upper ? sign : -sign;
-    const float4* p = row + (in ? upper ? l - readers : l : 0);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const float4 v = p[i * readers];
-      r.c[i] = in ? pack2(v.x, v.y) : pack2(1.f, 1.f);
-      r.s[i] = in ? pack2(v.z * sg, v.w * sg) : pack2(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = p[i * t.step];
+      r.c[i] = pack2(v.x, v.y);
+      r.s[i] = fmul2(pack2(v.z, v.w), t.sign);
     }
   } else {
-    const float4* p = row + (in ? l : 0);
+    // partner of the even feature: -sin, of the odd one: +sin (t.sign has the even one's)
+    float sg, unused;
+    unpack2(t.sign, sg, unused);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const float4 v = p[i * readers];
-      const float s0 = v.z * sign, s1 = v.w * sign;
-      r.c[2 * i] = in ? pack2(v.x, v.x) : pack2(1.f, 1.f);
-      r.c[2 * i + 1] = in ? pack2(v.y, v.y) : pack2(1.f, 1.f);
-      r.s[2 * i] = in ? pack2(-s0, s0) : pack2(0.f, 0.f);
-      r.s[2 * i + 1] = in ? pack2(-s1, s1) : pack2(0.f, 0.f);
+    for (int i = 0; i < 2; ++i) {
+      const float4 v = p[i * t.step];
+      r.c[2 * i] = pack2(v.x, v.x);
+      r.c[2 * i + 1] = pack2(v.y, v.y);
+      r.s[2 * i] = pack2(v.z * sg, -v.z * sg);
+      r.s[2 * i + 1] = pack2(v.w * sg, -v.w * sg);
     }
   }
 }
@@ -179,6 +194,18 @@ __device__ __forceinline__ void turn8(P4& p, const Turn& r, int src) {
       partner = pack2(hi, lo);
     p.v[i] = ffma2(partner, r.s[i], fmul2(p.v[i], r.c[i]));
   }
+}
+
+// The SFU's root and reciprocal: within a unit or two of the last place.
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int D>
@@ -230,7 +257,7 @@ struct Walk {
 
 template <typename T, int D, int kRot>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks) qk_kernel(const __grid_constant__ QkArgs a) {
-  __shared__ float4 turns[kRot == kRotNone ? 1 : kQkTokens * D / 4];
+  __shared__ float4 turns[kRot == kRotNone ? 1 : kQkTokens * D / 4 + 1];
   __shared__ double rate[kMaxRotPairs];   // the parameter bank would serialise the lanes' reads
   if (kRot != kRotNone && threadIdx.x < a.rot_dim / 2) rate[threadIdx.x] = a.rate[threadIdx.x];
   const int64_t first = (int64_t)blockIdx.x * a.tokens_per_block;
@@ -245,6 +272,8 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks) qk_kernel(const __gri
       sh[i] = load8(a.shift + at);
     }
   }
+  TurnPlace place{};
+  if (kRot != kRotNone) place = turn_place<kRot>(turns, kQkTokens * D / 4, s.l, a.rot_dim, 1.f);
   const T* zp = static_cast<const T*>(a.z) + (first * a.H + s.head) * D + 8 * s.l;
   const int64_t zrow = (int64_t)a.H * D;
   // z of this round and of the next
@@ -274,13 +303,12 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks) qk_kernel(const __gri
     P4 z = z0.get();
     z0 = z1;
     if (s.on && k + 2 * a.token_slots < len) z1.load(zp + (k + 2 * a.token_slots) * zrow);
-    const float nrm = sqrtf(row_sum<D>(dot8(z, z)));
-    const float inv = 1.f / (nrm < a.eps ? a.eps : nrm);
+    const float nrm = root(row_sum<D>(dot8(z, z)));
+    const float inv = reciprocal(nrm < a.eps ? a.eps : nrm);   // (a NaN stays)
 #pragma unroll
     for (int i = 0; i < 4; ++i) z.v[i] = fmul2(z.v[i], pack2(inv, inv));
     Turn turn;
-    if (kRot != kRotNone)
-      load_turn<kRot>(turn, turns + (on ? k - fill0 : 0) * (a.rot_dim / 4), s.l, a.rot_dim, 1.f);
+    if (kRot != kRotNone) load_turn<kRot>(turn, turns, place, on ? k - fill0 : 0);
     const int64_t at = w.row(a.H, a.T, s.head) * D + 8 * s.l;
     w.step(a.token_slots, a.T);
 #pragma unroll
@@ -323,25 +351,36 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const _
     for (int i = 0; i < 4; ++i) sc[i] = load8(a.scale + ((int64_t)i * a.H + s.head) * D + 8 * s.l);
   }
   const int len = (int)(last - first);
-  const int64_t zrow = (int64_t)a.H * D, z_at = (first * a.H + (s.on ? s.head : 0)) * D + 8 * s.l;
+  TurnPlace place{};
+  if (kRot != kRotNone) place = turn_place<kRot>(turns, kQkTokens * D / 4, s.l, a.rot_dim, -1.f);
+  const int64_t zrow = (int64_t)a.H * D;
+  const int head = s.on ? s.head : 0;
+  T* dz = static_cast<T*>(a.dz) + ((first + s.tsub) * a.H + head) * D + 8 * s.l;   // this round's
+  const T* z_next = static_cast<const T*>(a.z) + ((first + s.tsub) * a.H + head) * D + 8 * s.l;
   Walk w, w0;
   w0.start(first, a.T);
   w = w0;
   w.step(s.tsub, a.T);
+  int64_t at = w.row(a.H, a.T, head) * D + 8 * s.l;
   auto fetch = [&](int k, int stage) {   // in order of k
     uint4* to = ring + stage * 5 * kParts * kBwdThreads + threadIdx.x;
     const bool on = s.on && k < len;
-    const int64_t at = on ? w.row(a.H, a.T, s.head) * D + 8 * s.l : 0, z = on ? z_at + k * zrow : 0;
+    constexpr int kStep = 16 / sizeof(T);
 #pragma unroll
     for (int h = 0; h < kParts; ++h) {
-      constexpr int kStep = 16 / sizeof(T);
 #pragma unroll
       for (int o = 0; o < 4; ++o)
         copy16(to + (o * kParts + h) * kBwdThreads, static_cast<const T*>(a.dout[o]) + at + h * kStep, on);
-      copy16(to + (4 * kParts + h) * kBwdThreads, static_cast<const T*>(a.z) + z + h * kStep, on);
+      copy16(to + (4 * kParts + h) * kBwdThreads, z_next + h * kStep, on);
     }
     cp_async_commit();
-    w.step(a.token_slots, a.T);
+    z_next += a.token_slots * zrow;
+    w.t += a.token_slots;
+    at += a.token_slots * D;
+    if (w.t >= a.T) {
+      w.step(0, a.T);
+      at = w.row(a.H, a.T, head) * D + 8 * s.l;
+    }
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(s.tsub + i * a.token_slots, i);
@@ -376,14 +415,14 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const _
     }
     if (++stage == S) stage = 0;
     g.zero();
-    const float nrm = sqrtf(row_sum<D>(dot8(z, z)));
-    const float inv = 1.f / (nrm < a.eps ? a.eps : nrm);
+    const float nrm = root(row_sum<D>(dot8(z, z)));
+    const float inv = reciprocal(nrm < a.eps ? a.eps : nrm);   // (a NaN stays)
     const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) z.v[i] = fmul2(z.v[i], inv2);
     if (kRot != kRotNone) {
       Turn turn;
-      load_turn<kRot>(turn, turns + (on ? k - fill0 : 0) * (a.rot_dim / 4), s.l, a.rot_dim, -1.f);
+      load_turn<kRot>(turn, turns, place, on ? k - fill0 : 0);
       turn8<kRot>(p[0], turn, s.src);
       turn8<kRot>(p[1], turn, s.src);
     }
@@ -400,7 +439,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const _
     if (nrm <= a.eps) zg = 0.f;   // z' = z / eps there: no term through the norm
 #pragma unroll
     for (int i = 0; i < 4; ++i) g.v[i] = fmul2(ffma2(z.v[i], pack2(-zg, -zg), g.v[i]), inv2);
-    if (on) store8(static_cast<T*>(a.dz) + z_at + k * zrow, g);
+    if (on) store8(dz, g);
+    dz += a.token_slots * zrow;
   }
   cp_async_wait<0>();
   // The token slots' sums into the first slot's, in order, through the ring.
@@ -527,7 +567,7 @@ cudaError_t run(const QkProblem& p, const Plan& pl, bool backward, cudaStream_t 
     const auto kern = rot == kRotNone     ? qk_bwd_kernel<T, D, kRotNone>
                       : rot == kRotHalves ? qk_bwd_kernel<T, D, kRotHalves>
                                           : qk_bwd_kernel<T, D, kRotInterleaved>;
-    const int smem = kStages<T> * 5 * (int)sizeof(T) / 2 * kBwdThreads * 16 + kQkTokens * D / 4 * 16;
+    const int smem = kStages<T> * 5 * (int)sizeof(T) / 2 * kBwdThreads * 16 + (kQkTokens * D / 4 + 1) * 16;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     kern<<<grid, kBwdThreads, smem, st>>>(a);
   }
