@@ -370,7 +370,9 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
  * held in fp32.  A gate of log_a = -inf (or low enough that exp is 0), or a
  * document start at token t (reset), drops the first term: h_t = x_t.
  *
- *   x, log_a, y : [B, L, D] dtype `dtype`; y may equal x.
+ *   x, log_a, y : [B, L, D] dtype `dtype`; y may equal x.  log_a <= 0 is what
+ *                 the operator is for and is not checked; growing gates work
+ *                 as long as the product of any 512 in a row stays finite.
  *   reset       : [B, L] uint8 or NULL; non-zero = a document starts there.
  *   state_in    : [B, D] fp32 h_{-1}, or NULL for zero.
  *   state_out   : [B, D] fp32 receives h_{L-1}, or NULL; may equal state_in.

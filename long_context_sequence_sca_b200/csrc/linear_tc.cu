@@ -22,6 +22,8 @@
 // With CG = 2 a pair of CTAs shares one 256 x kBN tile: each loads its 128
 // rows of A and half the rows of B, so a k-block moves half the bytes per
 // multiply-add of a 128 x kBN tile; the even CTA issues the MMAs for both.
+#include <type_traits>
+
 #include "common.cuh"
 #include "gecko_internal.h"
 #include "linear.cuh"
@@ -526,6 +528,179 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   if (CG == 2) cluster_sync();
 }
 
+// Few rows (M <= 128; generation, short prompts): the product is bound by the
+// other operand's bytes, so the work is spread over as many SMs as it reaches:
+// tiles of 128 columns, and the depth shared by the CTAs of a cluster, each with
+// a run of the k-blocks (balanced, none empty).  Their sums meet through
+// distributed shared memory: each CTA leaves its rows in the memory of its (now
+// idle) stages and takes an equal share of the columns, adding the CTAs' parts
+// in rank order.  One launch, and no working memory.
+// What keeps the bytes coming is how many stages are on their way, so a stage
+// holds only the rows there are (to a multiple of 8): the MMA reads 128 all the
+// same, the others from the operand behind, and their results are not used.  (8 x
+// 4096 x 4096: 13.4 us with six whole stages, with eleven short ones 12.4.)
+constexpr int kFewN = 128;
+constexpr int kFewRing = 196608, kFewMostStages = 12;   // bytes of the ring
+constexpr int kFewPitch = kFewN + 4;   // floats per row left in shared memory
+constexpr int kFewMiscOff = kFewRing + (2 * kFewMostStages + 1) * 8;
+constexpr int kFewAlloc = kFewMiscOff + 16 + 1024;
+static_assert(128 * kFewPitch * 4 <= kFewRing, "the sums have to fit the stages");
+static_assert(kFewAlloc <= 232448, "shared memory above the per-block limit");
+
+// Rows of A in a stage.  (Stored along its rows, A comes in whole boxes.)
+__host__ __device__ constexpr int few_rows(int64_t M, bool mn) { return mn ? 128 : (int)((M + 7) / 8 * 8); }
+
+template <bool AMN, bool BMN, class Epi>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
+                                                                   const __grid_constant__ CUtensorMap mb,
+                                                                   const GemmShape g, const Epi ep, int* status) {
+  const int a_bytes = few_rows(g.M, AMN) * kBK * 2, stage = a_bytes + kFewN * kBK * 2;
+  const int NS = min(kFewMostStages, kFewRing / stage);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewRing);
+  uint64_t* empty = full + kFewMostStages;
+  uint64_t* acc_full = empty + kFewMostStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kFewMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kFewMiscOff + 4);
+  const int warp = warp_id_uniform(), lane = threadIdx.x % 32;
+  const int S = g.splits, rank = (int)cluster_rank(), n0 = (int)(blockIdx.x / S) * kFewN;
+  const int kb0 = g.k_blocks * rank / S, kb1 = g.k_blocks * (rank + 1) / S;
+  // one k-block of a plane product into a stage
+  auto load = [&](int s, int kb, int left) {
+    uint8_t *pa = smem + s * stage, *pb = pa + a_bytes;
+    const uint32_t bar = smem_u32(full + s);
+    const int za = plane_a(left), zb = plane_b(left);
+    mbar_arrive_expect_tx(full + s, stage);
+    if (AMN) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) tma_load<1>(pa + i * 8192, &ma, bar, 64 * i, kb * kBK, za);
+    } else {
+      tma_load<1>(pa, &ma, bar, kb * kBK, 0, za);
+    }
+    if (BMN) {
+#pragma unroll
+      for (int i = 0; i < kFewN / 64; ++i) tma_load<1>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK, zb);
+    } else {
+      tma_load<1>(pb, &mb, bar, kb * kBK, n0, zb);
+    }
+  };
+  const int blocks = (kb1 - kb0) * g.pairs;
+  int it = 0, kb = kb0, left = g.pairs - 1;   // the loading thread's place
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    // the first round of stages is on its way before anything else is set up
+    for (; it < NS && it < blocks; ++it) {
+      load(it, kb, left);
+      if (++kb == kb1) kb = kb0, --left;
+    }
+  }
+  if (warp == 2) tmem_take<1>(tmem_slot, kFewN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t phase = 0;   // of the wait for an emptied stage
+      for (int s = 0; it < blocks; ++it) {
+        if (!(ok = mbar_wait(empty + s, phase, abort_flag, status))) break;
+        load(s, kb, left);
+        if (++kb == kb1) kb = kb0, --left;
+        if (++s == NS) s = 0, phase ^= 1;
+      }
+      if (!ok)   // the copies issued land before the CTA exits
+        for (int i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait_drain(full + i % NS, (i / NS) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, kFewN, AMN, BMN);
+      const uint32_t base = smem_u32(smem);
+      uint32_t phase = 0;
+      for (int it = 0, s = 0; it < blocks; ++it) {
+        if (!mbar_wait(full + s, phase, abort_flag, status)) break;
+        tc_fence_after();
+        const uint32_t a0 = base + s * stage, b0 = a0 + a_bytes;
+        const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
+        const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          umma<1>(tmem, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)), idesc,
+                  it > 0 || kk > 0 ? 1u : 0u);
+        umma_done<1>(empty + s);
+        if (++s == NS) s = 0, phase ^= 1;
+      }
+      umma_done<1>(acc_full);   // also after an abort: what was issued is done before TMEM is given back
+      mbar_wait_drain(acc_full, 0);
+    }
+    __syncwarp();
+  } else if (warp >= kEpilogueWarp) {
+    const int q = warp % 4, half = (warp - kEpilogueWarp) / 4, m = q * 32 + lane;
+    if (__all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, status))) {
+      tc_fence_after();
+      float* to = reinterpret_cast<float*>(smem) + m * kFewPitch + half * (kFewN / 2);
+      for (int c = 0; c < kFewN / 2; c += 32) {
+        uint32_t v[32];
+        tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + half * (kFewN / 2) + c, v);
+        tmem_wait_ld();
+        if (m < g.M)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(to + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) tmem_give<1>(tmem, kFewN);
+  // this CTA's share of the columns, 128 / S: four at a time from every CTA into its own rows (nobody
+  // else reads those), then bands of 32 through the epilogue
+  float* own = reinterpret_cast<float*>(smem) + rank * (kFewN / S);
+  const int quads = kFewN / 4 / S, bands = kFewN / 32 / S;
+  for (int i = threadIdx.x; i < (int)g.M * quads && S > 1; i += kGemmThreads) {
+    const int m = i / quads;
+    float4* at = reinterpret_cast<float4*>(own + m * kFewPitch) + (i - m * quads);
+    float4 w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < S)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(w[r].x), "=f"(w[r].y), "=f"(w[r].z), "=f"(w[r].w)
+                     : "r"(map_to(at, r))
+                     : "memory");
+    float4 v = w[0];
+#pragma unroll
+    for (int r = 1; r < 4; ++r)
+      if (r < S) v.x += w[r].x, v.y += w[r].y, v.z += w[r].z, v.w += w[r].w;
+    *at = v;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (int)g.M * bands; i += kGemmThreads) {
+    const int m = i / bands, c = (i - m * bands) * 32, n = n0 + rank * (kFewN / S) + c;
+    if (n >= g.N || *abort_flag) continue;
+    typename Epi::Fetched f;
+    const int64_t row = ep.row(m);
+    ep.fetch(f, row, n, true);
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 w = *reinterpret_cast<const float4*>(own + m * kFewPitch + c + j);
+      v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
+    }
+    ep.put(f, row, n, 0, v);
+  }
+  cluster_sync();   // the others have read this CTA's memory
+}
+
 // Sum of the parts' sums, then the epilogue: a thread takes 32 columns of a row.
 template <class Epi>
 __global__ void __launch_bounds__(128) gemm_sum_kernel(const float* part, int splits, int64_t M, int N, const Epi ep) {
@@ -590,31 +765,52 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int planes, int64_t rows,
 }
 
 struct GemmPlan {
-  int cg;
+  int cg;        // CTAs per tile; 0: the few-rows kernel
+  bool sum;      // the accumulator's runs are added up in registers (kSum)
   GemmShape g;
 };
 
-GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes) {
+// exact: the sums of the accumulator's runs are to be rounded, not cut (a part
+// of one run needs no adding up).
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   GemmPlan pl;
   auto tiles = [](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
+  GemmShape& g = pl.g;
+  g.M = M;
+  g.N = N;
+  g.tiles_n = tiles(N, kBN);
+  g.k_blocks = tiles(K, kBK);
+  g.pairs = planes == 3 ? kPairs : 1;
+  g.run = planes == 3 ? 16 : 32;
+  if (M <= 128) {
+    // Parts of two k-blocks at least, and clusters that are all resident at once
+    // (33 of 4, 74 of 2: cudaOccupancyMaxActiveClusters); more would run in a
+    // second wave (16 of 8 CTAs where 15 fit: 20 us against 14).
+    const int few_tiles = tiles(N, kFewN);
+    const int S = few_tiles <= 33 && g.k_blocks >= 8 ? 4 : few_tiles <= 74 && g.k_blocks >= 4 ? 2 : 1;
+    if (!exact || tiles(g.k_blocks, S) * g.pairs <= g.run) {
+      pl.cg = 0;
+      pl.sum = false;
+      g.tiles_m = 1;
+      g.tiles_n = few_tiles;
+      g.splits = S;
+      g.blocks_per_split = 0;
+      return pl;
+    }
+  }
   pl.cg = M <= 128 ? 1 : 2;
-  pl.g.M = M;
-  pl.g.N = N;
-  pl.g.tiles_m = tiles(M, 128 * pl.cg);
-  pl.g.tiles_n = tiles(N, kBN);
-  pl.g.k_blocks = tiles(K, kBK);
-  pl.g.pairs = planes == 3 ? kPairs : 1;
-  pl.g.run = planes == 3 ? 16 : 32;
+  g.tiles_m = tiles(M, 128 * pl.cg);
   // Few tiles: as many parts as fill the GPU, each of eight k-blocks' work at
   // least (below 32 the second kernel costs more than the parts save).
-  const int64_t slots = sm_count() / pl.cg, t = (int64_t)pl.g.tiles_m * pl.g.tiles_n;
-  const int64_t work = (int64_t)pl.g.k_blocks * pl.g.pairs;   // k-blocks of a tile
+  const int64_t slots = sm_count() / pl.cg, t = (int64_t)g.tiles_m * g.tiles_n;
+  const int64_t work = (int64_t)g.k_blocks * g.pairs;   // k-blocks of a tile
   int64_t splits = work < 32 ? 1 : slots / t;
   if (splits > work / 8) splits = work / 8;
-  if (splits > pl.g.k_blocks) splits = pl.g.k_blocks;
+  if (splits > g.k_blocks) splits = g.k_blocks;
   if (splits < 1) splits = 1;
-  pl.g.blocks_per_split = (int)((pl.g.k_blocks + splits - 1) / splits);
-  pl.g.splits = (pl.g.k_blocks + pl.g.blocks_per_split - 1) / pl.g.blocks_per_split;
+  g.blocks_per_split = (int)((g.k_blocks + splits - 1) / splits);
+  g.splits = (g.k_blocks + g.blocks_per_split - 1) / g.blocks_per_split;
+  pl.sum = exact && g.blocks_per_split * g.pairs > g.run;
   return pl;
 }
 
@@ -625,61 +821,67 @@ EpiPlain<T> plain(void* c, int64_t M, int64_t N) {
   return {static_cast<T*>(c), M, (int)N, aligned32(c) && N * sizeof(T) % 32 == 0};
 }
 
-template <int CG, bool AMN, bool BMN, bool kSum, class Epi>
-cudaError_t run_gemm(const GemmPlan& pl, const void* A, const void* B, int64_t K, int planes, const Epi& ep,
-                     int* status, cudaStream_t st) {
-  using Cfg = GemmCfg<CG>;
-  CUtensorMap ma, mb;
-  cudaError_t e;
-  const GemmShape& g = pl.g;
-  if ((e = AMN ? make_map(&ma, A, planes, K, g.M, kBK) : make_map(&ma, A, planes, g.M, K, 128))) return e;
-  if ((e = BMN ? make_map(&mb, B, planes, K, g.N, kBK) : make_map(&mb, B, planes, g.N, K, kBN / CG))) return e;
-  auto kern = gemm_tc_kernel<CG, AMN, BMN, kSum, Epi>;
-  static const int regs = [&] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
-  }();
-  if (kSum && 128 * kRegsCtl + 256 * kRegsEpilogue > kGemmThreads * regs) return cudaErrorInvalidConfiguration;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kAlloc))) return e;
-  const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
-  const int64_t slots = sm_count() / CG;
+template <class Kernel, class Epi>
+cudaError_t launch_gemm(Kernel kern, int ctas, int cluster, int smem, const CUtensorMap& ma, const CUtensorMap& mb,
+                        const GemmShape& g, const Epi& ep, int* status, cudaStream_t st) {
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(CG * (units < slots ? units : slots)));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = Cfg::kAlloc;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, g, ep, status);
 }
 
-template <bool AMN, bool BMN, bool kSum, class Epi>
-cudaError_t gemm_of(const GemmPlan& pl, const void* A, const void* B, int64_t K, int planes, const Epi& ep,
-                    int* status, cudaStream_t st) {
-  return pl.cg == 2 ? run_gemm<2, AMN, BMN, kSum, Epi>(pl, A, B, K, planes, ep, status, st)
-                    : run_gemm<1, AMN, BMN, kSum, Epi>(pl, A, B, K, planes, ep, status, st);
+template <int CG, bool AMN, bool BMN, bool kSum, class Epi>
+cudaError_t run_gemm(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& ep, int* status,
+                     cudaStream_t st) {
+  const GemmShape& g = pl.g;
+  auto kern = gemm_tc_kernel<CG, AMN, BMN, kSum, Epi>;
+  static const int regs = [&] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (kSum && 128 * kRegsCtl + 256 * kRegsEpilogue > kGemmThreads * regs) return cudaErrorInvalidConfiguration;
+  const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits, slots = sm_count() / CG;
+  return launch_gemm(kern, (int)(CG * (units < slots ? units : slots)), CG, GemmCfg<CG>::kAlloc, ma, mb, g, ep, status,
+                     st);
 }
 
-// A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.  kExact: the
-// sums of the accumulator's runs are rounded, not cut (a part of one run needs
-// no adding up).
+// A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.
 template <bool AMN, bool BMN, bool kExact, class Epi>
 cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, int planes, const Epi& ep, void* ws,
                  int* status, cudaStream_t st) {
-  const GemmPlan pl = gemm_plan(M, N, K, planes);
-  const bool sum = kExact && pl.g.blocks_per_split * pl.g.pairs > pl.g.run;
-  auto product = [&](const auto& e) {
-    if constexpr (kExact)
-      if (sum) return gemm_of<AMN, BMN, true>(pl, A, B, K, planes, e, status, st);
-    return gemm_of<AMN, BMN, false>(pl, A, B, K, planes, e, status, st);
+  const GemmPlan pl = gemm_plan(M, N, K, planes, kExact);
+  CUtensorMap ma, mb;
+  cudaError_t e;
+  const int b_rows = pl.cg == 2 ? kBN / 2 : pl.cg == 1 ? kBN : kFewN;
+  if ((e = AMN ? make_map(&ma, A, planes, K, M, kBK)
+               : make_map(&ma, A, planes, M, K, pl.cg == 0 ? few_rows(M, false) : 128))) return e;
+  if ((e = BMN ? make_map(&mb, B, planes, K, N, kBK) : make_map(&mb, B, planes, N, K, b_rows))) return e;
+  if (pl.cg == 0)
+    return launch_gemm(gemm_few_kernel<AMN, BMN, Epi>, pl.g.tiles_n * pl.g.splits, pl.g.splits, kFewAlloc, ma, mb, pl.g,
+                       ep, status, st);
+  auto product = [&](const auto& out) -> cudaError_t {
+    using Out = std::decay_t<decltype(out)>;
+    if constexpr (kExact) {
+      if (pl.sum)
+        return pl.cg == 2 ? run_gemm<2, AMN, BMN, true, Out>(pl, ma, mb, out, status, st)
+                          : run_gemm<1, AMN, BMN, true, Out>(pl, ma, mb, out, status, st);
+      // (one CTA per tile: only where the few-rows kernel would not be exact)
+      if (pl.cg == 1) return run_gemm<1, AMN, BMN, false, Out>(pl, ma, mb, out, status, st);
+    }
+    return run_gemm<2, AMN, BMN, false, Out>(pl, ma, mb, out, status, st);
   };
   if (pl.g.splits == 1) return product(ep);
   float* part = static_cast<float*>(ws);
-  if (cudaError_t e = product(EpiPlain<float>{part, M, (int)N, aligned32(part)})) return e;
+  if ((e = product(EpiPlain<float>{part, M, (int)N, aligned32(part)}))) return e;
   gemm_sum_kernel<Epi><<<(unsigned)((M * ((N + 31) / 32) + 127) / 128), 128, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
   return cudaGetLastError();
 }
@@ -697,8 +899,8 @@ cudaError_t forward_tc(const LinearProblem& p, const void* x, const void* w, voi
 }  // namespace
 
 size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
-  const GemmPlan pl = gemm_plan(M, N, K, dtype == kBF16 ? 1 : 3);
-  return pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
+  const GemmPlan pl = gemm_plan(M, N, K, dtype == kBF16 ? 1 : 3, true);
+  return pl.cg == 0 || pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st) {

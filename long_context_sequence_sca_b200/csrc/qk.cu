@@ -508,7 +508,8 @@ Plan plan_of(int64_t n_tokens, int64_t H, int64_t d, int threads, int blocks_per
   const int64_t slots = threads / (d / 8);
   Plan pl;
   double best = 0.0;
-  for (int64_t n = (H + slots - 1) / slots; n <= H; ++n) {
+  const int64_t least = (H + slots - 1) / slots;
+  for (int64_t n = least; n <= H && n < least + 16; ++n) {
     const int64_t heads = (H + n - 1) / n, tokens = slots / heads;
     const double used = (double)H * tokens / (double)(n * slots);
     if (used > best + 0.05) {   // more blocks fill the sine table more often

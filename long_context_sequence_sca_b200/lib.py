@@ -752,6 +752,10 @@ def linear_backward(x, w, dy, pre=None, act: str = "none", heads: int = 0, need=
     return dx, dw, db
 
 
+# Autograd wrappers.  To capture a backward pass into a CUDA graph, follow
+# torch's rules for whole-network capture: warm up on a side stream, and let no
+# eager graph of the same leaves live on while capturing.
+
 class GatedScanFunction(torch.autograd.Function):
     """torch.autograd wrapper: (y, state) = GatedScanFunction.apply(x, log_a,
     state_in or None, reset or None)."""
