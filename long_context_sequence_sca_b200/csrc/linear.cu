@@ -100,6 +100,7 @@ constexpr int kDuCols = 256;     // columns per block: 32 threads x 8
 constexpr int kDuRowsPar = 8;    // rows per round of a block
 constexpr int kDuUnroll = 4;     // rounds whose loads are in flight together
 constexpr int kDuBlocks = 4;     // per SM
+constexpr int kDuOneBlock = 128;    // up to this many rows, one block of rows and no second kernel for db
 
 // du = dy f'(u), [M, N] row-major in the tensors' type (for bf16 one rounding, to
 // the operand type of the two products that follow) or as bf16 planes; the
@@ -185,6 +186,7 @@ int64_t du_row_blocks(int64_t M, int64_t N) {
   int64_t blocks = (int64_t)kDuBlocks * sm_count() / cols;
   if (blocks < 1) blocks = 1;
   if (blocks > 65535) blocks = 65535;
+  if (M <= kDuOneBlock) return 1;
   const int64_t most = (M + kDuUnroll * kDuRowsPar - 1) / (kDuUnroll * kDuRowsPar);
   return blocks < most ? blocks : most;
 }
@@ -204,18 +206,27 @@ void launch_du(const LinearProblem& p, void* du, float* part, int64_t blocks, cu
     linear_du_kernel<T, kActGelu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
 }
 
-// The bf16 planes of n fp32 values (n a multiple of 8).
-__global__ void __launch_bounds__(256) split_kernel(const float* v, __nv_bfloat16* planes, int64_t n) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
+// The bf16 planes of one or two runs of fp32 values (their numbers multiples of 8).
+struct SplitArgs {
+  const float* v[2];
+  __nv_bfloat16* planes[2];
+  int64_t n[2];
+};
+__global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
+  int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int which = i >= a.n[0];
+  if (which) i -= a.n[0];
+  if (i >= a.n[which]) return;
   float w[8];
-  load_f8(v + i, w);
-  store_planes(planes + i, n, w);
+  load_f8(a.v[which] + i, w);
+  store_planes(a.planes[which] + i, a.n[which], w);
 }
 
-void launch_split(const void* v, void* planes, int64_t n, cudaStream_t st) {
-  split_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, st>>>(static_cast<const float*>(v),
-                                                               static_cast<__nv_bfloat16*>(planes), n);
+void launch_split(const void* v0, void* p0, int64_t n0, const void* v1, void* p1, int64_t n1, cudaStream_t st) {
+  const SplitArgs a{{static_cast<const float*>(v0), static_cast<const float*>(v1)},
+                    {static_cast<__nv_bfloat16*>(p0), static_cast<__nv_bfloat16*>(p1)},
+                    {n0, n1}};
+  split_kernel<<<(unsigned)(((n0 + n1) / 8 + 255) / 256), 256, 0, st>>>(a);
 }
 
 // GECKO_KERNELS=simt selects the CUDA-core kernels for every type.
@@ -271,8 +282,7 @@ cudaError_t forward_impl(const LinearProblem& p, cudaStream_t st) {
   const Layout l = layout_of(p, false);
   char* ws = static_cast<char*>(p.ws);
   if (p.dtype == kBF16) return launch_linear_tc(p, p.x, p.w, ws + l.gemm, st);
-  launch_split(p.x, ws + l.x, p.M() * p.K, st);
-  launch_split(p.w, ws + l.w, p.N * p.K, st);
+  launch_split(p.x, ws + l.x, p.M() * p.K, p.w, ws + l.w, p.N * p.K, st);
   return launch_linear_tc(p, ws + l.x, ws + l.w, ws + l.gemm, st);
 }
 
@@ -288,9 +298,10 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   if (p.db || (!alias && products)) {
     const int64_t blocks = du_row_blocks(M, p.N);
     void* du = products && !alias ? ws + l.du : nullptr;
-    if (tc && f32) launch_du<T, true>(p, du, p.db ? part : nullptr, blocks, st);
-    else launch_du<T, false>(p, du, p.db ? part : nullptr, blocks, st);
-    if (p.db) linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
+    float* sums = !p.db ? nullptr : blocks == 1 ? p.db : part;   // one block of rows: its sums are db
+    if (tc && f32) launch_du<T, true>(p, du, sums, blocks, st);
+    else launch_du<T, false>(p, du, sums, blocks, st);
+    if (p.db && blocks > 1) linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
   }
   const void* g = alias ? p.dy : ws + l.du;
   if (!tc) {
@@ -299,8 +310,11 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
     return cudaGetLastError();
   }
   const void *x = p.x, *w = p.w;
-  if (f32 && p.dx) launch_split(p.w, ws + l.w, p.N * p.K, st), w = ws + l.w;
-  if (f32 && p.dw) launch_split(p.x, ws + l.x, M * p.K, st), x = ws + l.x;
+  if (f32 && products) {
+    launch_split(p.x, ws + l.x, p.dw ? M * p.K : 0, p.w, ws + l.w, p.dx ? p.N * p.K : 0, st);
+    x = ws + l.x;
+    w = ws + l.w;
+  }
   cudaError_t e;
   if (p.dx && (e = launch_linear_dx_tc(p, g, w, ws + l.gemm, st))) return e;
   if (p.dw && (e = launch_linear_dw_tc(p, g, x, ws + l.gemm, st))) return e;

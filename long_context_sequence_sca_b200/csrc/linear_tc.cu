@@ -528,9 +528,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   if (CG == 2) cluster_sync();
 }
 
-// Few rows (M <= 128; generation, short prompts): the product is bound by the
-// other operand's bytes, so the work is spread over as many SMs as it reaches:
-// tiles of 128 columns, and the depth shared by the CTAs of a cluster, each with
+// Few rows (generation, short prompts) or few tiles: the product is bound by the
+// other operand's bytes, or by how long a tile takes, so the work is spread over
+// as many SMs as it reaches: tiles of 128 x 128, one per cluster, and the depth
+// shared by the cluster's CTAs, each with
 // a run of the k-blocks (balanced, none empty).  Their sums meet through
 // distributed shared memory: each CTA leaves its rows in the memory of its (now
 // idle) stages and takes an equal share of the columns, adding the CTAs' parts
@@ -548,7 +549,9 @@ static_assert(128 * kFewPitch * 4 <= kFewRing, "the sums have to fit the stages"
 static_assert(kFewAlloc <= 232448, "shared memory above the per-block limit");
 
 // Rows of A in a stage.  (Stored along its rows, A comes in whole boxes.)
-__host__ __device__ constexpr int few_rows(int64_t M, bool mn) { return mn ? 128 : (int)((M + 7) / 8 * 8); }
+__host__ __device__ constexpr int few_rows(int64_t M, bool mn) {
+  return mn || M > 120 ? 128 : (int)((M + 7) / 8 * 8);
+}
 
 template <bool AMN, bool BMN, class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
@@ -564,7 +567,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kFewMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kFewMiscOff + 4);
   const int warp = warp_id_uniform(), lane = threadIdx.x % 32;
-  const int S = g.splits, rank = (int)cluster_rank(), n0 = (int)(blockIdx.x / S) * kFewN;
+  const int S = g.splits, rank = (int)cluster_rank(), tile = blockIdx.x / S;
+  const int n0 = tile / g.tiles_m * kFewN, m0 = tile % g.tiles_m * 128;   // (tiles of one column band together)
+  const int rows = (int)min((int64_t)128, g.M - m0);
   const int kb0 = g.k_blocks * rank / S, kb1 = g.k_blocks * (rank + 1) / S;
   // one k-block of a plane product into a stage
   auto load = [&](int s, int kb, int left) {
@@ -574,9 +579,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     mbar_arrive_expect_tx(full + s, stage);
     if (AMN) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) tma_load<1>(pa + i * 8192, &ma, bar, 64 * i, kb * kBK, za);
+      for (int i = 0; i < 2; ++i) tma_load<1>(pa + i * 8192, &ma, bar, m0 + 64 * i, kb * kBK, za);
     } else {
-      tma_load<1>(pa, &ma, bar, kb * kBK, 0, za);
+      tma_load<1>(pa, &ma, bar, kb * kBK, m0, za);
     }
     if (BMN) {
 #pragma unroll
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
         uint32_t v[32];
         tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + half * (kFewN / 2) + c, v);
         tmem_wait_ld();
-        if (m < g.M)
+        if (m < rows)
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<uint4*>(to + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   // else reads those), then bands of 32 through the epilogue
   float* own = reinterpret_cast<float*>(smem) + rank * (kFewN / S);
   const int quads = kFewN / 4 / S, bands = kFewN / 32 / S;
-  for (int i = threadIdx.x; i < (int)g.M * quads && S > 1; i += kGemmThreads) {
+  for (int i = threadIdx.x; i < rows * quads && S > 1; i += kGemmThreads) {
     const int m = i / quads;
     float4* at = reinterpret_cast<float4*>(own + m * kFewPitch) + (i - m * quads);
     float4 w[4];
@@ -684,11 +689,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     *at = v;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < (int)g.M * bands; i += kGemmThreads) {
+  for (int i = threadIdx.x; i < rows * bands; i += kGemmThreads) {
     const int m = i / bands, c = (i - m * bands) * 32, n = n0 + rank * (kFewN / S) + c;
     if (n >= g.N || *abort_flag) continue;
     typename Epi::Fetched f;
-    const int64_t row = ep.row(m);
+    const int64_t row = ep.row(m0 + m);
     ep.fetch(f, row, n, true);
     float v[32];
 #pragma unroll
@@ -770,8 +775,9 @@ struct GemmPlan {
   GemmShape g;
 };
 
-// exact: the sums of the accumulator's runs are to be rounded, not cut (a part
-// of one run needs no adding up).
+// exact: the sums of the accumulator's runs are to be rounded, not cut.  A part
+// of one run needs no adding up (of fp32, one run of the last plane product: the
+// ones before it are small).
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   GemmPlan pl;
   auto tiles = [](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
@@ -782,26 +788,11 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   g.k_blocks = tiles(K, kBK);
   g.pairs = planes == 3 ? kPairs : 1;
   g.run = planes == 3 ? 16 : 32;
-  if (M <= 128) {
-    // Parts of two k-blocks at least, and clusters that are all resident at once
-    // (33 of 4, 74 of 2: cudaOccupancyMaxActiveClusters); more would run in a
-    // second wave (16 of 8 CTAs where 15 fit: 20 us against 14).
-    const int few_tiles = tiles(N, kFewN);
-    const int S = few_tiles <= 33 && g.k_blocks >= 8 ? 4 : few_tiles <= 74 && g.k_blocks >= 4 ? 2 : 1;
-    if (!exact || tiles(g.k_blocks, S) * g.pairs <= g.run) {
-      pl.cg = 0;
-      pl.sum = false;
-      g.tiles_m = 1;
-      g.tiles_n = few_tiles;
-      g.splits = S;
-      g.blocks_per_split = 0;
-      return pl;
-    }
-  }
+  // Large tiles.  Few of them: as many parts as fill the GPU, each of eight
+  // k-blocks' work at least (below 32 the second kernel costs more than the
+  // parts save).
   pl.cg = M <= 128 ? 1 : 2;
   g.tiles_m = tiles(M, 128 * pl.cg);
-  // Few tiles: as many parts as fill the GPU, each of eight k-blocks' work at
-  // least (below 32 the second kernel costs more than the parts save).
   const int64_t slots = sm_count() / pl.cg, t = (int64_t)g.tiles_m * g.tiles_n;
   const int64_t work = (int64_t)g.k_blocks * g.pairs;   // k-blocks of a tile
   int64_t splits = work < 32 ? 1 : slots / t;
@@ -810,7 +801,29 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   if (splits < 1) splits = 1;
   g.blocks_per_split = (int)((g.k_blocks + splits - 1) / splits);
   g.splits = (g.k_blocks + g.blocks_per_split - 1) / g.blocks_per_split;
-  pl.sum = exact && g.blocks_per_split * g.pairs > g.run;
+  pl.sum = exact && g.blocks_per_split > g.run;
+
+  // Or the small tiles of the few-rows kernel, whose clusters are to be resident
+  // all at once (33 of 4 CTAs, 74 of 2: cudaOccupancyMaxActiveClusters; 16 of 8
+  // where 15 fit took 20 us against 14).  In k-blocks of about 0.3 us, what the
+  // large tiles cost beyond their own is 16 and one per part for the second
+  // kernel, or 8 without one (measured on 22 shapes from 256 x 256 x 16384 to
+  // 2000 x 264 x 72; 1024 x 1024 x 1024: 9.9 us against 12.2, 777 x 520 x 1032 in
+  // fp32, where the small tiles do not split enough, 32.3 against 25.7).
+  const int64_t few_tiles = (int64_t)tiles(M, 128) * tiles(N, kFewN);
+  if (M <= 128 || few_tiles <= sm_count()) {
+    const int S = few_tiles <= 33 && g.k_blocks >= 8 ? 4 : few_tiles <= 74 && g.k_blocks >= 4 ? 2 : 1;
+    const int64_t few = (int64_t)tiles(g.k_blocks, S) * g.pairs;
+    const int64_t large = (int64_t)g.blocks_per_split * g.pairs + (g.splits > 1 ? 16 + g.splits : 8);
+    if ((!exact || tiles(g.k_blocks, S) <= g.run) && (M <= 128 || few <= large)) {
+      pl.cg = 0;
+      pl.sum = false;
+      g.tiles_m = tiles(M, 128);
+      g.tiles_n = tiles(N, kFewN);
+      g.splits = S;
+      g.blocks_per_split = 0;
+    }
+  }
   return pl;
 }
 
@@ -866,7 +879,7 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, 
                : make_map(&ma, A, planes, M, K, pl.cg == 0 ? few_rows(M, false) : 128))) return e;
   if ((e = BMN ? make_map(&mb, B, planes, K, N, kBK) : make_map(&mb, B, planes, N, K, b_rows))) return e;
   if (pl.cg == 0)
-    return launch_gemm(gemm_few_kernel<AMN, BMN, Epi>, pl.g.tiles_n * pl.g.splits, pl.g.splits, kFewAlloc, ma, mb, pl.g,
+    return launch_gemm(gemm_few_kernel<AMN, BMN, Epi>, pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, pl.g.splits, kFewAlloc, ma, mb, pl.g,
                        ep, status, st);
   auto product = [&](const auto& out) -> cudaError_t {
     using Out = std::decay_t<decltype(out)>;

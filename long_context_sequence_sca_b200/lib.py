@@ -671,7 +671,8 @@ def qk_forward(z, scale, shift, eps: float = 1e-6, rot_dim: int = 0, rot_base: f
     dev = z.device
     _tensor(_required(shift, "shift"), "shift", (4, H, d), torch.float32, dev)
     with _on(dev, stream) as st:
-        outs = tuple([z.new_empty((B, H, T, d)) for _ in range(4)])
+        q = z.new_empty((B, H, T, d))
+        outs = (q, torch.empty_like(q), torch.empty_like(q), torch.empty_like(q))
         _check(gecko_qk_forward(z.data_ptr(), scale.data_ptr(), shift.data_ptr(), _ptr(pos),
                                 *(o.data_ptr() for o in outs), B, T, H, d, eps, pos0, rot_dim, rot_base,
                                 int(interleaved), _DT[z.dtype], st))
