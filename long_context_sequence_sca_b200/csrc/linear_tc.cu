@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
 
 // Few rows (generation, short prompts) or few tiles: the product is bound by the
 // other operand's bytes, or by how long a tile takes, so the work is spread over
-// as many SMs as it reaches: tiles of 128 x 128, one per cluster, and the depth
+// as many SMs as it reaches: tiles of 128 x FN, one per cluster, and the depth
 // shared by the cluster's CTAs, each with
 // a run of the k-blocks (balanced, none empty).  Their sums meet through
 // distributed shared memory: each CTA leaves its rows in the memory of its (now
@@ -540,12 +540,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
 // holds only the rows there are (to a multiple of 8): the MMA reads 128 all the
 // same, the others from the operand behind, and their results are not used.  (8 x
 // 4096 x 4096: 13.4 us with six whole stages, with eleven short ones 12.4.)
-constexpr int kFewN = 128;
 constexpr int kFewRing = 196608, kFewMostStages = 12;   // bytes of the ring
-constexpr int kFewPitch = kFewN + 4;   // floats per row left in shared memory
+template <int FN> constexpr int kFewPitch = FN + 4;     // floats per row left in shared memory
 constexpr int kFewMiscOff = kFewRing + (2 * kFewMostStages + 1) * 8;
 constexpr int kFewAlloc = kFewMiscOff + 16 + 1024;
-static_assert(128 * kFewPitch * 4 <= kFewRing, "the sums have to fit the stages");
+static_assert(128 * kFewPitch<256> * 4 <= kFewRing, "the sums have to fit the stages");
 static_assert(kFewAlloc <= 232448, "shared memory above the per-block limit");
 
 // Rows of A in a stage.  (Stored along its rows, A comes in whole boxes.)
@@ -553,11 +552,11 @@ __host__ __device__ constexpr int few_rows(int64_t M, bool mn) {
   return mn || M > 120 ? 128 : (int)((M + 7) / 8 * 8);
 }
 
-template <bool AMN, bool BMN, class Epi>
+template <int FN, bool AMN, bool BMN, class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
                                                                    const __grid_constant__ CUtensorMap mb,
                                                                    const GemmShape g, const Epi ep, int* status) {
-  const int a_bytes = few_rows(g.M, AMN) * kBK * 2, stage = a_bytes + kFewN * kBK * 2;
+  const int a_bytes = few_rows(g.M, AMN) * kBK * 2, stage = a_bytes + FN * kBK * 2;
   const int NS = min(kFewMostStages, kFewRing / stage);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kFewMiscOff + 4);
   const int warp = warp_id_uniform(), lane = threadIdx.x % 32;
   const int S = g.splits, rank = (int)cluster_rank(), tile = blockIdx.x / S;
-  const int n0 = tile / g.tiles_m * kFewN, m0 = tile % g.tiles_m * 128;   // (tiles of one column band together)
+  const int n0 = tile / g.tiles_m * FN, m0 = tile % g.tiles_m * 128;   // (tiles of one column band together)
   const int rows = (int)min((int64_t)128, g.M - m0);
   const int kb0 = g.k_blocks * rank / S, kb1 = g.k_blocks * (rank + 1) / S;
   // one k-block of a plane product into a stage
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     }
     if (BMN) {
 #pragma unroll
-      for (int i = 0; i < kFewN / 64; ++i) tma_load<1>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK, zb);
+      for (int i = 0; i < FN / 64; ++i) tma_load<1>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK, zb);
     } else {
       tma_load<1>(pb, &mb, bar, kb * kBK, n0, zb);
     }
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
       if (++kb == kb1) kb = kb0, --left;
     }
   }
-  if (warp == 2) tmem_take<1>(tmem_slot, kFewN);
+  if (warp == 2) tmem_take<1>(tmem_slot, FN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, kFewN, AMN, BMN);
+      constexpr uint32_t idesc = idesc_bf16_f32(128, FN, AMN, BMN);
       const uint32_t base = smem_u32(smem);
       uint32_t phase = 0;
       for (int it = 0, s = 0; it < blocks; ++it) {
@@ -651,10 +650,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     const int q = warp % 4, half = (warp - kEpilogueWarp) / 4, m = q * 32 + lane;
     if (__all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, status))) {
       tc_fence_after();
-      float* to = reinterpret_cast<float*>(smem) + m * kFewPitch + half * (kFewN / 2);
-      for (int c = 0; c < kFewN / 2; c += 32) {
+      float* to = reinterpret_cast<float*>(smem) + m * kFewPitch<FN> + half * (FN / 2);
+      for (int c = 0; c < FN / 2; c += 32) {
         uint32_t v[32];
-        tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + half * (kFewN / 2) + c, v);
+        tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + half * (FN / 2) + c, v);
         tmem_wait_ld();
         if (m < rows)
 #pragma unroll
@@ -666,14 +665,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 2) tmem_give<1>(tmem, kFewN);
-  // this CTA's share of the columns, 128 / S: four at a time from every CTA into its own rows (nobody
+  if (warp == 2) tmem_give<1>(tmem, FN);
+  // this CTA's share of the columns, FN / S: four at a time from every CTA into its own rows (nobody
   // else reads those), then bands of 32 through the epilogue
-  float* own = reinterpret_cast<float*>(smem) + rank * (kFewN / S);
-  const int quads = kFewN / 4 / S, bands = kFewN / 32 / S;
+  float* own = reinterpret_cast<float*>(smem) + rank * (FN / S);
+  const int quads = FN / 4 / S, bands = FN / 32 / S;
   for (int i = threadIdx.x; i < rows * quads && S > 1; i += kGemmThreads) {
     const int m = i / quads;
-    float4* at = reinterpret_cast<float4*>(own + m * kFewPitch) + (i - m * quads);
+    float4* at = reinterpret_cast<float4*>(own + m * kFewPitch<FN>) + (i - m * quads);
     float4 w[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -690,7 +689,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   }
   __syncthreads();
   for (int i = threadIdx.x; i < rows * bands; i += kGemmThreads) {
-    const int m = i / bands, c = (i - m * bands) * 32, n = n0 + rank * (kFewN / S) + c;
+    const int m = i / bands, c = (i - m * bands) * 32, n = n0 + rank * (FN / S) + c;
     if (n >= g.N || *abort_flag) continue;
     typename Epi::Fetched f;
     const int64_t row = ep.row(m0 + m);
@@ -698,7 +697,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const float4 w = *reinterpret_cast<const float4*>(own + m * kFewPitch + c + j);
+      const float4 w = *reinterpret_cast<const float4*>(own + m * kFewPitch<FN> + c + j);
       v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
     }
     ep.put(f, row, n, 0, v);
@@ -771,6 +770,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int planes, int64_t rows,
 
 struct GemmPlan {
   int cg;        // CTAs per tile; 0: the few-rows kernel
+  int few_n;     // and its tiles' columns
   bool sum;      // the accumulator's runs are added up in registers (kSum)
   GemmShape g;
 };
@@ -803,26 +803,31 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   g.splits = (g.k_blocks + g.blocks_per_split - 1) / g.blocks_per_split;
   pl.sum = exact && g.blocks_per_split > g.run;
 
-  // Or the small tiles of the few-rows kernel, whose clusters are to be resident
-  // all at once (33 of 4 CTAs, 74 of 2: cudaOccupancyMaxActiveClusters; 16 of 8
-  // where 15 fit took 20 us against 14).  In k-blocks of about 0.3 us, what the
-  // large tiles cost beyond their own is 16 and one per part for the second
-  // kernel, or 8 without one (measured on 22 shapes from 256 x 256 x 16384 to
-  // 2000 x 264 x 72; 1024 x 1024 x 1024: 9.9 us against 12.2, 777 x 520 x 1032 in
-  // fp32, where the small tiles do not split enough, 32.3 against 25.7).
-  const int64_t few_tiles = (int64_t)tiles(M, 128) * tiles(N, kFewN);
-  if (M <= 128 || few_tiles <= sm_count()) {
-    const int S = few_tiles <= 33 && g.k_blocks >= 8 ? 4 : few_tiles <= 74 && g.k_blocks >= 4 ? 2 : 1;
-    const int64_t few = (int64_t)tiles(g.k_blocks, S) * g.pairs;
-    const int64_t large = (int64_t)g.blocks_per_split * g.pairs + (g.splits > 1 ? 16 + g.splits : 8);
-    if ((!exact || tiles(g.k_blocks, S) <= g.run) && (M <= 128 || few <= large)) {
-      pl.cg = 0;
-      pl.sum = false;
-      g.tiles_m = tiles(M, 128);
-      g.tiles_n = tiles(N, kFewN);
-      g.splits = S;
-      g.blocks_per_split = 0;
-    }
+  // Or the few-rows kernel's tiles, of 128 or 256 columns, whose clusters are to be
+  // resident all at once (33 of 4 CTAs, 74 of 2: cudaOccupancyMaxActiveClusters; 16
+  // of 8 where 15 fit took 20 us against 14).  The times in us that decide were
+  // fitted to 28 products from 8 x 4096 x 4096 to 3711 x 1000 x 1288, bf16 and
+  // fp32: 256 x 4096 x 4096 takes 20.5 with large tiles, 17.3 and 15.8 with these;
+  // 1024 x 1024 x 1024 12.2, 10.2 and 11.9; 1024 x 4096 x 4096 27.7, 27.3 and 31.2.
+  const int64_t waves = (t * g.splits + slots - 1) / slots;
+  double best = (g.splits > 1 ? 14.0 + 0.5 * g.splits : 7.5) + 0.29 * g.blocks_per_split * g.pairs * waves;
+  const int64_t k_blocks = g.k_blocks;
+  for (int n : {128, 256}) {
+    const int64_t few_tiles = (int64_t)tiles(M, 128) * tiles(N, n);
+    if (few_tiles > sm_count() && (M > 128 || n == 256)) continue;
+    const int S = few_tiles <= 33 && k_blocks >= 8 ? 4 : few_tiles <= 74 && k_blocks >= 4 ? 2 : 1;
+    if (exact && tiles(k_blocks, S) > g.run) continue;
+    const double work_part = (double)tiles(k_blocks, S) * g.pairs;
+    const double cost = n == 128 ? 6.3 + 0.325 * work_part : 9.0 + 0.36 * work_part;
+    if (cost > best && !(M <= 128 && pl.cg != 0)) continue;   // (one-CTA large tiles only where it must be)
+    best = cost;
+    pl.cg = 0;
+    pl.few_n = n;
+    pl.sum = false;
+    g.tiles_m = tiles(M, 128);
+    g.tiles_n = tiles(N, n);
+    g.splits = S;
+    g.blocks_per_split = 0;
   }
   return pl;
 }
@@ -874,12 +879,13 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, 
   const GemmPlan pl = gemm_plan(M, N, K, planes, kExact);
   CUtensorMap ma, mb;
   cudaError_t e;
-  const int b_rows = pl.cg == 2 ? kBN / 2 : pl.cg == 1 ? kBN : kFewN;
+  const int b_rows = pl.cg == 2 ? kBN / 2 : pl.cg == 1 ? kBN : pl.few_n;
   if ((e = AMN ? make_map(&ma, A, planes, K, M, kBK)
                : make_map(&ma, A, planes, M, K, pl.cg == 0 ? few_rows(M, false) : 128))) return e;
   if ((e = BMN ? make_map(&mb, B, planes, K, N, kBK) : make_map(&mb, B, planes, N, K, b_rows))) return e;
   if (pl.cg == 0)
-    return launch_gemm(gemm_few_kernel<AMN, BMN, Epi>, pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, pl.g.splits, kFewAlloc, ma, mb, pl.g,
+    return launch_gemm(pl.few_n == 128 ? gemm_few_kernel<128, AMN, BMN, Epi> : gemm_few_kernel<256, AMN, BMN, Epi>,
+                       pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, pl.g.splits, kFewAlloc, ma, mb, pl.g,
                        ep, status, st);
   auto product = [&](const auto& out) -> cudaError_t {
     using Out = std::decay_t<decltype(out)>;
@@ -890,6 +896,7 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, 
       // (one CTA per tile: only where the few-rows kernel would not be exact)
       if (pl.cg == 1) return run_gemm<1, AMN, BMN, false, Out>(pl, ma, mb, out, status, st);
     }
+    if (pl.cg != 2) return cudaErrorInvalidValue;   // (the maps are made for pl.cg)
     return run_gemm<2, AMN, BMN, false, Out>(pl, ma, mb, out, status, st);
   };
   if (pl.g.splits == 1) return product(ep);

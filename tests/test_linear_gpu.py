@@ -69,7 +69,8 @@ def check(L, inp, dtype, act, H):
 SIZES = [(1, 1, 8, 8, 0), (1, 3, 24, 16, 0), (2, 65, 136, 72, 0), (5, 1, 64, 200, 8), (3, 129, 264, 520, 3),
          (1, 300, 1000, 1288, 0), (8, 1, 512, 1024, 4), (33, 1, 256, 264, 2), (2, 64, 128, 64, 1), (1, 500, 512, 256, 4),
          (3, 257, 640, 136, 5), (1, 2000, 264, 72, 0), (1, 17, 2048, 136, 16), (1, 130, 72, 5000, 0), (1, 5003, 16, 24, 2),
-         (1, 100, 136, 5000, 0), (1, 128, 520, 128, 0), (2, 3, 2056, 200, 0), (1, 9, 24, 10000, 0)]
+         (1, 100, 136, 5000, 0), (1, 128, 520, 128, 0), (2, 3, 2056, 200, 0), (1, 9, 24, 10000, 0),
+         (1, 300, 1032, 2560, 0), (3, 171, 512, 1544, 4), (1, 1100, 264, 520, 0)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
