@@ -290,6 +290,10 @@ struct LinearProblem {
 size_t linear_workspace_bytes(const LinearProblem& p, bool backward);
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st);
 cudaError_t launch_linear_bwd(const LinearProblem& p, cudaStream_t st);
+// Elements between the rows of an fp32 operand's bf16 planes: whole 128-byte lines
+// (with rows of 1032 elements, each 128-byte load touched two).
+inline int64_t plane_pitch(int64_t inner) { return (inner + 63) / 64 * 64; }
+
 // Tensor-core (tcgen05) products.  The operands are p's, or du, for bf16; their
 // three bf16 planes for fp32.  ws: gemm_tc_workspace of the product's rows,
 // columns and depth.

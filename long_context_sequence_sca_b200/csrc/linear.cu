@@ -107,7 +107,8 @@ constexpr int kDuOneBlock = 128;    // up to this many rows, one block of rows a
 // column sums of the unrounded values go to part [gridDim.y, N].
 template <typename T, int kAct, bool kPlanes>
 __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, const float* pre, void* du, float* part,
-                                                                   OutLayout lay, int64_t M, int64_t N, int64_t rows) {
+                                                                   OutLayout lay, int64_t M, int64_t N, int64_t rows,
+                                                                   int64_t pitch) {
   __shared__ float red[kDuRowsPar][kDuCols];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int64_t n = (int64_t)blockIdx.x * kDuCols + cx * 8;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
             for (int j = 0; j < 8; ++j) v[j] *= act_slope(w[j], kAct);
           }
           if (du) {
-            if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + mi * N + n, M * N, v);
+            if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + mi * pitch + n, M * pitch, v);
             else store_f8(static_cast<T*>(du) + mi * N + n, v);
           }
 #pragma unroll
@@ -198,35 +199,44 @@ void launch_du(const LinearProblem& p, void* du, float* part, int64_t blocks, cu
   const T* dy = static_cast<const T*>(p.dy);
   const float* pre = p.pre;
   const OutLayout lay(p);
+  const int64_t pitch = plane_pitch(p.N);   // (planes)
   if (p.act == kActNone)
-    linear_du_kernel<T, kActNone, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+    linear_du_kernel<T, kActNone, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows, pitch);
   else if (p.act == kActSilu)
-    linear_du_kernel<T, kActSilu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+    linear_du_kernel<T, kActSilu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows, pitch);
   else
-    linear_du_kernel<T, kActGelu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows);
+    linear_du_kernel<T, kActGelu, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows, pitch);
 }
 
-// The bf16 planes of one or two runs of fp32 values (their numbers multiples of 8).
+// The bf16 planes of one or two fp32 matrices [rows, inner] (inner a multiple of 8).
 struct SplitArgs {
   const float* v[2];
   __nv_bfloat16* planes[2];
-  int64_t n[2];
+  int64_t rows[2];
+  uint32_t inner;
+  int64_t pitch;
 };
 __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
-  int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  const int which = i >= a.n[0];
-  if (which) i -= a.n[0];
-  if (i >= a.n[which]) return;
+  const uint32_t per_row = a.inner / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  int64_t r = i / per_row;
+  const uint32_t c = (uint32_t)(i - r * per_row) * 8;
+  const int which = r >= a.rows[0];
+  if (which) r -= a.rows[0];
+  if (r >= a.rows[which]) return;
   float w[8];
-  load_f8(a.v[which] + i, w);
-  store_planes(a.planes[which] + i, a.n[which], w);
+  load_f8(a.v[which] + r * a.inner + c, w);
+  store_planes(a.planes[which] + r * a.pitch + c, a.rows[which] * a.pitch, w);
 }
 
-void launch_split(const void* v0, void* p0, int64_t n0, const void* v1, void* p1, int64_t n1, cudaStream_t st) {
+void launch_split(const void* v0, void* p0, int64_t rows0, const void* v1, void* p1, int64_t rows1, int64_t inner,
+                  cudaStream_t st) {
   const SplitArgs a{{static_cast<const float*>(v0), static_cast<const float*>(v1)},
                     {static_cast<__nv_bfloat16*>(p0), static_cast<__nv_bfloat16*>(p1)},
-                    {n0, n1}};
-  split_kernel<<<(unsigned)(((n0 + n1) / 8 + 255) / 256), 256, 0, st>>>(a);
+                    {rows0, rows1},
+                    (uint32_t)inner,
+                    plane_pitch(inner)};
+  split_kernel<<<(unsigned)(((rows0 + rows1) * (inner / 8) + 255) / 256), 256, 0, st>>>(a);
 }
 
 // GECKO_KERNELS=simt selects the CUDA-core kernels for every type.
@@ -242,7 +252,9 @@ struct Layout {
   size_t du, part, x, w, gemm, bytes;
 };
 
-size_t plane_bytes(int64_t n) { return up256(3 * sizeof(__nv_bfloat16) * (size_t)n); }
+size_t plane_bytes(int64_t rows, int64_t inner) {
+  return up256(3 * sizeof(__nv_bfloat16) * (size_t)rows * plane_pitch(inner));
+}
 
 Layout layout_of(const LinearProblem& p, bool backward) {
   const int64_t M = p.M();
@@ -257,11 +269,11 @@ Layout layout_of(const LinearProblem& p, bool backward) {
   l.dy_is_du = !f32 && p.act == kActNone && p.H == 0;
   if (backward) {
     // planes take more than the fp32 values
-    l.du = take(l.dy_is_du ? 0 : f32 ? plane_bytes(M * p.N) : 2 * (size_t)M * p.N);
+    l.du = take(l.dy_is_du ? 0 : f32 ? plane_bytes(M, p.N) : 2 * (size_t)M * p.N);
     l.part = take(sizeof(float) * du_row_blocks(M, p.N) * p.N);
   }
-  l.x = take(f32 ? plane_bytes(M * p.K) : 0);
-  l.w = take(f32 ? plane_bytes(p.N * p.K) : 0);
+  l.x = take(f32 ? plane_bytes(M, p.K) : 0);
+  l.w = take(f32 ? plane_bytes(p.N, p.K) : 0);
   size_t g = backward ? gemm_tc_workspace(M, p.K, p.N, p.dtype) : gemm_tc_workspace(M, p.N, p.K, p.dtype);
   if (backward) {
     const size_t dw = gemm_tc_workspace(p.N, p.K, M, p.dtype);
@@ -282,7 +294,7 @@ cudaError_t forward_impl(const LinearProblem& p, cudaStream_t st) {
   const Layout l = layout_of(p, false);
   char* ws = static_cast<char*>(p.ws);
   if (p.dtype == kBF16) return launch_linear_tc(p, p.x, p.w, ws + l.gemm, st);
-  launch_split(p.x, ws + l.x, p.M() * p.K, p.w, ws + l.w, p.N * p.K, st);
+  launch_split(p.x, ws + l.x, p.M(), p.w, ws + l.w, p.N, p.K, st);
   return launch_linear_tc(p, ws + l.x, ws + l.w, ws + l.gemm, st);
 }
 
@@ -311,7 +323,7 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   }
   const void *x = p.x, *w = p.w;
   if (f32 && products) {
-    launch_split(p.x, ws + l.x, p.dw ? M * p.K : 0, p.w, ws + l.w, p.dx ? p.N * p.K : 0, st);
+    launch_split(p.x, ws + l.x, p.dw ? M : 0, p.w, ws + l.w, p.dx ? p.N : 0, p.K, st);
     x = ws + l.x;
     w = ws + l.w;
   }

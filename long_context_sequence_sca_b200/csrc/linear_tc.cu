@@ -753,13 +753,14 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// `planes` of [rows, inner] bf16 row-major, boxes of 64 x box_rows with 128-byte
-// swizzle; what lies outside a plane reads as zero.
+// `planes` of [rows, inner] bf16 row-major (three planes: rows plane_pitch(inner)
+// apart), boxes of 64 x box_rows with 128-byte swizzle; what lies outside a plane reads as zero.
 cudaError_t make_map(CUtensorMap* m, const void* base, int planes, int64_t rows, int64_t inner, int box_rows) {
+  const int64_t pitch = planes == 1 ? inner : plane_pitch(inner);
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
-  cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)(rows * inner) * 2};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(rows * pitch) * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
