@@ -290,7 +290,7 @@ struct LinearProblem {
 size_t linear_workspace_bytes(const LinearProblem& p, bool backward);
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t st);
 cudaError_t launch_linear_bwd(const LinearProblem& p, cudaStream_t st);
-// Elements between the rows of an fp32 operand's bf16 planes: whole 128-byte lines
+// Elements between the rows of du, and of an fp32 operand's bf16 planes: whole 128-byte lines
 // (with rows of 1032 elements, each 128-byte load touched two).
 inline int64_t plane_pitch(int64_t inner) { return (inner + 63) / 64 * 64; }
 
@@ -299,7 +299,9 @@ inline int64_t plane_pitch(int64_t inner) { return (inner + 63) / 64 * 64; }
 // columns and depth.
 size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype);
 cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st);
-cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, const void* w, void* ws, cudaStream_t st);
-cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, const void* x, void* ws, cudaStream_t st);
+cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, int64_t du_pitch, const void* w, void* ws,
+                                cudaStream_t st);
+cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, int64_t du_pitch, const void* x, void* ws,
+                                cudaStream_t st);
 
 }  // namespace gecko

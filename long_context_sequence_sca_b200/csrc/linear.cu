@@ -102,7 +102,7 @@ constexpr int kDuUnroll = 4;     // rounds whose loads are in flight together
 constexpr int kDuBlocks = 4;     // per SM
 constexpr int kDuOneBlock = 128;    // up to this many rows, one block of rows and no second kernel for db
 
-// du = dy f'(u), [M, N] row-major in the tensors' type (for bf16 one rounding, to
+// du = dy f'(u), [M, N] with rows `pitch` apart in the tensors' type (for bf16 one rounding, to
 // the operand type of the two products that follow) or as bf16 planes; the
 // column sums of the unrounded values go to part [gridDim.y, N].
 template <typename T, int kAct, bool kPlanes>
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
           }
           if (du) {
             if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + mi * pitch + n, M * pitch, v);
-            else store_f8(static_cast<T*>(du) + mi * N + n, v);
+            else store_f8(static_cast<T*>(du) + mi * pitch + n, v);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] += v[j];
@@ -193,13 +193,12 @@ int64_t du_row_blocks(int64_t M, int64_t N) {
 }
 
 template <typename T, bool kPlanes>
-void launch_du(const LinearProblem& p, void* du, float* part, int64_t blocks, cudaStream_t st) {
+void launch_du(const LinearProblem& p, void* du, int64_t pitch, float* part, int64_t blocks, cudaStream_t st) {
   const dim3 grid((unsigned)((p.N + kDuCols - 1) / kDuCols), (unsigned)blocks);
   const int64_t rows = (p.M() + blocks - 1) / blocks;
   const T* dy = static_cast<const T*>(p.dy);
   const float* pre = p.pre;
   const OutLayout lay(p);
-  const int64_t pitch = plane_pitch(p.N);   // (planes)
   if (p.act == kActNone)
     linear_du_kernel<T, kActNone, kPlanes><<<grid, 256, 0, st>>>(dy, pre, du, part, lay, p.M(), p.N, rows, pitch);
   else if (p.act == kActSilu)
@@ -269,7 +268,7 @@ Layout layout_of(const LinearProblem& p, bool backward) {
   l.dy_is_du = !f32 && p.act == kActNone && p.H == 0;
   if (backward) {
     // planes take more than the fp32 values
-    l.du = take(l.dy_is_du ? 0 : f32 ? plane_bytes(M, p.N) : 2 * (size_t)M * p.N);
+    l.du = take(l.dy_is_du ? 0 : f32 ? plane_bytes(M, p.N) : 2 * (size_t)M * plane_pitch(p.N));
     l.part = take(sizeof(float) * du_row_blocks(M, p.N) * p.N);
   }
   l.x = take(f32 ? plane_bytes(M, p.K) : 0);
@@ -307,12 +306,13 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   float* part = reinterpret_cast<float*>(ws + l.part);
   const bool tc = use_tc(), products = p.dx || p.dw;
   const bool alias = tc ? l.dy_is_du : p.act == kActNone && p.H == 0;
+  const int64_t pitch = tc && !alias ? plane_pitch(p.N) : p.N;   // of du
   if (p.db || (!alias && products)) {
     const int64_t blocks = du_row_blocks(M, p.N);
     void* du = products && !alias ? ws + l.du : nullptr;
     float* sums = !p.db ? nullptr : blocks == 1 ? p.db : part;   // one block of rows: its sums are db
-    if (tc && f32) launch_du<T, true>(p, du, sums, blocks, st);
-    else launch_du<T, false>(p, du, sums, blocks, st);
+    if (tc && f32) launch_du<T, true>(p, du, pitch, sums, blocks, st);
+    else launch_du<T, false>(p, du, pitch, sums, blocks, st);
     if (p.db && blocks > 1) linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
   }
   const void* g = alias ? p.dy : ws + l.du;
@@ -328,8 +328,8 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
     w = ws + l.w;
   }
   cudaError_t e;
-  if (p.dx && (e = launch_linear_dx_tc(p, g, w, ws + l.gemm, st))) return e;
-  if (p.dw && (e = launch_linear_dw_tc(p, g, x, ws + l.gemm, st))) return e;
+  if (p.dx && (e = launch_linear_dx_tc(p, g, pitch, w, ws + l.gemm, st))) return e;
+  if (p.dw && (e = launch_linear_dw_tc(p, g, pitch, x, ws + l.gemm, st))) return e;
   return cudaGetLastError();
 }
 

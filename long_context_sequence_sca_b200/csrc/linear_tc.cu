@@ -753,10 +753,16 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// `planes` of [rows, inner] bf16 row-major (three planes: rows plane_pitch(inner)
-// apart), boxes of 64 x box_rows with 128-byte swizzle; what lies outside a plane reads as zero.
-cudaError_t make_map(CUtensorMap* m, const void* base, int planes, int64_t rows, int64_t inner, int box_rows) {
-  const int64_t pitch = planes == 1 ? inner : plane_pitch(inner);
+struct Operand {
+  const void* p;
+  int64_t pitch;   // elements between rows
+};
+
+// `planes` of [rows, inner] bf16 row-major, boxes of 64 x box_rows with 128-byte
+// swizzle; what lies outside a plane reads as zero.
+cudaError_t make_map(CUtensorMap* m, const Operand& o, int planes, int64_t rows, int64_t inner, int box_rows) {
+  const void* base = o.p;
+  const int64_t pitch = o.pitch;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
@@ -875,8 +881,8 @@ cudaError_t run_gemm(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMa
 
 // A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.
 template <bool AMN, bool BMN, bool kExact, class Epi>
-cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, int planes, const Epi& ep, void* ws,
-                 int* status, cudaStream_t st) {
+cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, int planes, const Epi& ep,
+                 void* ws, int* status, cudaStream_t st) {
   const GemmPlan pl = gemm_plan(M, N, K, planes, kExact);
   CUtensorMap ma, mb;
   cudaError_t e;
@@ -907,8 +913,14 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const void* A, const void* B, 
   return cudaGetLastError();
 }
 
+// x or w: rows of the tensor, or of its planes.
+Operand operand(const LinearProblem& p, const void* at, int64_t inner) {
+  return {at, p.dtype == kBF16 ? inner : plane_pitch(inner)};
+}
+
 template <typename T>
-cudaError_t forward_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st) {
+cudaError_t forward_tc(const LinearProblem& p, const void* xp, const void* wp, void* ws, cudaStream_t st) {
+  const Operand x = operand(p, xp, p.K), w = operand(p, wp, p.K);
   const int64_t run = p.H ? p.N / p.H : p.N;   // contiguous columns
   const EpiForward<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act,
                          aligned32(p.y) && run % 16 == 0, aligned32(p.pre)};
@@ -928,7 +940,9 @@ cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* 
   return p.dtype == kBF16 ? forward_tc<__nv_bfloat16>(p, x, w, ws, st) : forward_tc<float>(p, x, w, ws, st);
 }
 
-cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, const void* w, void* ws, cudaStream_t st) {
+cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* dup, int64_t du_pitch, const void* wp, void* ws,
+                                cudaStream_t st) {
+  const Operand du{dup, du_pitch}, w = operand(p, wp, p.K);
   if (p.dtype == kBF16)
     return gemm<false, true, false>(p.M(), p.K, p.N, du, w, 1, plain<__nv_bfloat16>(p.dx, p.M(), p.K),
                                     ws, p.status, st);
@@ -936,7 +950,9 @@ cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, const vo
                            p.status, st);
 }
 
-cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, const void* x, void* ws, cudaStream_t st) {
+cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* dup, int64_t du_pitch, const void* xp, void* ws,
+                                cudaStream_t st) {
+  const Operand du{dup, du_pitch}, x = operand(p, xp, p.K);
   if (p.dtype == kBF16)
     return gemm<true, true, false>(p.N, p.K, p.M(), du, x, 1, plain<__nv_bfloat16>(p.dw, p.N, p.K),
                                    ws, p.status, st);
