@@ -94,12 +94,88 @@ void simt_gemm(const void* A, int64_t am, int64_t ak, const void* B, int64_t bn,
                                                       bk, M, N, K, ep);
 }
 
+// ------------------------------------------------- few rows, fp32, forward --
+
+// Up to 16 rows of fp32: the weights' bytes are all there is to it, and splitting
+// them into planes would move them three times (8 x 4096 x 4096: 64 us that way,
+// 22.7 this way, 10 at HBM's rate).  A warp takes two columns of y (rows of w),
+// 16 bytes of each per lane and load; x comes by 512 of the depth through shared
+// memory, the next piece under way while one is used.
+constexpr int kRowsMost = 16, kRowsDepth = 512, kRowsWarps = 8, kRowsCols = 2 * kRowsWarps;
+
+template <int kM>
+__global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const float* x, const float* w, int M, int64_t N,
+                                                                      int64_t K, ForwardOut<float> ep) {
+  extern __shared__ float4 xs[];   // [2][kM][kRowsDepth / 4]
+  constexpr int kQ = kRowsDepth / 4;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int64_t n0 = (int64_t)blockIdx.x * kRowsCols + 2 * warp;
+  auto bring = [&](int64_t k0, int buf) {
+    for (int i = threadIdx.x; i < kM * kQ; i += 32 * kRowsWarps) {
+      const int m = i / kQ;
+      const int64_t k = k0 + (i - m * kQ) * 4;
+      const bool on = m < M && k < K;
+      copy16(xs + buf * kM * kQ + i, x + (on ? m * K + k : 0), on);
+    }
+    cp_async_commit();
+  };
+  float acc[2][kM] = {};
+  bring(0, 0);
+  int buf = 0;
+  for (int64_t k0 = 0; k0 < K; k0 += kRowsDepth, buf ^= 1) {
+    float4 v[2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t k = k0 + j * 128 + lane * 4;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        v[c][j] = n0 + c < N && k < K ? *reinterpret_cast<const float4*>(w + (n0 + c) * K + k)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    bring(k0 + kRowsDepth, buf ^ 1);   // (beyond K: zeros)
+    cp_async_wait<1>();
+    __syncthreads();
+    const float4* at = xs + buf * kM * kQ + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const float4 a = at[m * kQ + j * 32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          acc[c][m] = fmaf(a.x, v[c][j].x, fmaf(a.y, v[c][j].y, fmaf(a.z, v[c][j].z, fmaf(a.w, v[c][j].w, acc[c][m]))));
+      }
+    __syncthreads();   // the piece after next overwrites this one
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[c][m] += __shfl_xor_sync(0xffffffffu, acc[c][m], o);
+      if (lane == (c * kM + m) % 32 && m < M && n0 + c < N) ep(m, n0 + c, acc[c][m]);
+    }
+}
+
+template <int kM>
+cudaError_t launch_rows(const LinearProblem& p, const ForwardOut<float>& ep, cudaStream_t st) {
+  constexpr int smem = 2 * kM * kRowsDepth * 4;
+  if (cudaError_t e = cudaFuncSetAttribute(linear_rows_kernel<kM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+    return e;
+  linear_rows_kernel<kM><<<(unsigned)((p.N + kRowsCols - 1) / kRowsCols), 32 * kRowsWarps, smem, st>>>(
+      static_cast<const float*>(p.x), static_cast<const float*>(p.w), (int)p.M(), p.N, p.K, ep);
+  return cudaGetLastError();
+}
+
 // ----------------------------------------------------- gradient of u, db --
 
 constexpr int kDuCols = 256;     // columns per block: 32 threads x 8
 constexpr int kDuRowsPar = 8;    // rows per round of a block
-constexpr int kDuUnroll = 4;     // rounds whose loads are in flight together
-constexpr int kDuBlocks = 4;     // per SM
+// Blocks per SM.  With four rounds of loads in flight per thread the compiler
+// spilled (69 us for 8192 x 4096 SiLU with db; two rounds and three blocks 37,
+// one round and four blocks 37).
+constexpr int kDuBlocks = 4;
 constexpr int kDuOneBlock = 128;    // up to this many rows, one block of rows and no second kernel for db
 
 // du = dy f'(u), [M, N] with rows `pitch` apart in the tensors' type (for bf16 one rounding, to
@@ -116,37 +192,38 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
   float acc[8] = {};
   if (n < N) {
     const int64_t col = lay.col((int)n);
-    for (int64_t m = (int64_t)blockIdx.y * rows + ry; m < m1; m += kDuRowsPar * kDuUnroll) {
-      Vec8<T> g[kDuUnroll];
-      Vec8<float> u[kDuUnroll];
+    int64_t m = (int64_t)blockIdx.y * rows + ry;
+    // where row m begins; the next row of this thread is kDuRowsPar on
+    int64_t at = lay.row(m) + col;
+    uint32_t t = lay.H ? (uint32_t)m % lay.T : 0;
+    const int64_t step = (int64_t)kDuRowsPar * (lay.H ? lay.hd : N);
+    auto next = [&](int64_t to) {
+      at += step;
+      t += kDuRowsPar;
+      if (lay.H && t >= lay.T) {
+        t = (uint32_t)to % lay.T;
+        at = lay.row(to) + col;
+      }
+    };
+    for (; m < m1; m += kDuRowsPar) {
+      Vec8<T> g;
+      Vec8<float> u;
+      g.load(dy + at);
+      if (kAct != kActNone) u.load(pre + at);
+      next(m + kDuRowsPar);
+      float v[8], w[8];
+      g.get(v);
+      if (kAct != kActNone) {
+        u.get(w);
 #pragma unroll
-      for (int i = 0; i < kDuUnroll; ++i) {
-        const int64_t mi = m + i * kDuRowsPar;
-        if (mi < m1) {
-          const int64_t at = lay.row(mi) + col;
-          g[i].load(dy + at);
-          if (kAct != kActNone) u[i].load(pre + at);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], act_slope(w[j], kAct));   // (not fused into the sum below)
+      }
+      if (du) {
+        if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + m * pitch + n, M * pitch, v);
+        else store_f8(static_cast<T*>(du) + m * pitch + n, v);
       }
 #pragma unroll
-      for (int i = 0; i < kDuUnroll; ++i) {
-        const int64_t mi = m + i * kDuRowsPar;
-        if (mi < m1) {
-          float v[8], w[8];
-          g[i].get(v);
-          if (kAct != kActNone) {
-            u[i].get(w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= act_slope(w[j], kAct);
-          }
-          if (du) {
-            if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + mi * pitch + n, M * pitch, v);
-            else store_f8(static_cast<T*>(du) + mi * pitch + n, v);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] += v[j];
-        }
-      }
+      for (int j = 0; j < 8; ++j) acc[j] += v[j];
     }
   }
   if (!part) return;
@@ -181,14 +258,14 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int r
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Blocks of rows of the du pass: one wave, each with a few rounds at least.
+// Blocks of rows of the du pass: one wave, each with four rounds at least.
 int64_t du_row_blocks(int64_t M, int64_t N) {
   const int64_t cols = (N + kDuCols - 1) / kDuCols;
   int64_t blocks = (int64_t)kDuBlocks * sm_count() / cols;
   if (blocks < 1) blocks = 1;
   if (blocks > 65535) blocks = 65535;
   if (M <= kDuOneBlock) return 1;
-  const int64_t most = (M + kDuUnroll * kDuRowsPar - 1) / (kDuUnroll * kDuRowsPar);
+  const int64_t most = (M + 31) / 32;
   return blocks < most ? blocks : most;
 }
 
@@ -271,6 +348,7 @@ Layout layout_of(const LinearProblem& p, bool backward) {
     l.du = take(l.dy_is_du ? 0 : f32 ? plane_bytes(M, p.N) : 2 * (size_t)M * plane_pitch(p.N));
     l.part = take(sizeof(float) * du_row_blocks(M, p.N) * p.N);
   }
+  if (!backward && f32 && M <= kRowsMost) return l;   // no planes
   l.x = take(f32 ? plane_bytes(M, p.K) : 0);
   l.w = take(f32 ? plane_bytes(p.N, p.K) : 0);
   size_t g = backward ? gemm_tc_workspace(M, p.K, p.N, p.dtype) : gemm_tc_workspace(M, p.N, p.K, p.dtype);
@@ -285,8 +363,13 @@ Layout layout_of(const LinearProblem& p, bool backward) {
 
 template <typename T>
 cudaError_t forward_impl(const LinearProblem& p, cudaStream_t st) {
+  ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act};
+  if constexpr (sizeof(T) == 4)
+    if (p.M() <= kRowsMost)
+      return p.M() <= 4   ? launch_rows<4>(p, ep, st)
+             : p.M() <= 8 ? launch_rows<8>(p, ep, st)
+                          : launch_rows<16>(p, ep, st);
   if (!use_tc()) {
-    ForwardOut<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act};
     simt_gemm<T>(p.x, p.K, 1, p.w, p.K, 1, p.M(), p.N, p.K, ep, st);
     return cudaGetLastError();
   }

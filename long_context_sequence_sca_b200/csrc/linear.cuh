@@ -70,6 +70,12 @@ __device__ __forceinline__ void store_f8(__nv_bfloat16* p, const float (&v)[8]) 
                                             pack_bf16x2(v[6], v[7]));
 }
 
+// 16 bytes to shared memory without a stop in registers, or zeros.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+
 // v = h + m + l in bf16: each plane is the rest of the ones before it rounded to
 // nearest, so what is left is below 2^-25 |v|.  h is cut instead where rounding
 // would carry a finite v to infinity; an infinite v has no rest.
