@@ -357,7 +357,8 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
  * the current device (reset: any alignment) and every tensor is contiguous.
  * Outputs are fully overwritten and must not alias inputs or each other
  * except where stated.  Execution is asynchronous on `stream`; argument errors
- * are found on the host before anything is launched or written.  Returns
+ * are found on the host before anything is launched or written; a wait inside a
+ * kernel that runs out is reported by gecko_device_status().  Returns
  * GECKO_OK, GECKO_ERR_ARG (also a workspace that is too small),
  * GECKO_ERR_SHAPE, GECKO_ERR_ALIGN or GECKO_ERR_CUDA.
  */

@@ -618,8 +618,8 @@ def gated_scan_forward(x, log_a, reset=None, state_in=None, return_state=False, 
     with _on(dev, stream) as st:
         if y is None:
             y = torch.empty_like(x)
-        state = torch.empty((B, D), dtype=torch.float32, device=dev) if return_state else None
-        chunks = torch.empty((B, -(-L // SCAN_CHUNK), D), dtype=torch.float32, device=dev) if keep_chunks else None
+        state = torch.empty(B, D, dtype=torch.float32, device=dev) if return_state else None
+        chunks = torch.empty(B, -(-L // SCAN_CHUNK), D, dtype=torch.float32, device=dev) if keep_chunks else None
         ws, wp, wn = _workspace(gecko_gated_scan_workspace, (B, L, D, _DT[x.dtype], 0), dev)
         _check(gecko_gated_scan_forward(x.data_ptr(), log_a.data_ptr(), y.data_ptr(), _ptr(reset), _ptr(state_in),
                                         _ptr(state), _ptr(chunks), B, L, D, _DT[x.dtype], wp, wn, st))
@@ -641,7 +641,7 @@ def gated_scan_backward(x, log_a, dy, chunk_state, reset=None, dstate_out=None, 
     _tensor(dstate_out, "dstate_out", (B, D), torch.float32, dev)
     with _on(dev, stream) as st:
         dx, dg = torch.empty_like(x), torch.empty_like(x)
-        ds = torch.empty((B, D), dtype=torch.float32, device=dev)
+        ds = torch.empty(B, D, dtype=torch.float32, device=dev)
         ws, wp, wn = _workspace(gecko_gated_scan_workspace, (B, L, D, _DT[x.dtype], 1), dev)
         _check(gecko_gated_scan_backward(x.data_ptr(), log_a.data_ptr(), dy.data_ptr(), _ptr(reset),
                                          chunk_state.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dg.data_ptr(),
@@ -671,7 +671,7 @@ def qk_forward(z, scale, shift, eps: float = 1e-6, rot_dim: int = 0, rot_base: f
     dev = z.device
     _tensor(_required(shift, "shift"), "shift", (4, H, d), torch.float32, dev)
     with _on(dev, stream) as st:
-        q = z.new_empty((B, H, T, d))
+        q = torch.empty(B, H, T, d, dtype=z.dtype, device=dev)
         outs = (q, torch.empty_like(q), torch.empty_like(q), torch.empty_like(q))
         _check(gecko_qk_forward(z.data_ptr(), scale.data_ptr(), shift.data_ptr(), _ptr(pos),
                                 *(o.data_ptr() for o in outs), B, T, H, d, eps, pos0, rot_dim, rot_base,
@@ -727,8 +727,8 @@ def linear_forward(x, w, bias=None, residual=None, act: str = "none", heads: int
     _tensor(y, "y", shape, x.dtype, dev)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=dev)
-        pre = torch.empty(shape, dtype=torch.float32, device=dev) if keep_pre else None
+            y = torch.empty(*shape, dtype=x.dtype, device=dev)
+        pre = torch.empty(*shape, dtype=torch.float32, device=dev) if keep_pre else None
         ws, wp, wn = _workspace(gecko_linear_workspace, (B, T, N, K, heads, ACTS[act], _DT[x.dtype], 0), dev)
         _check(gecko_linear_forward(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre),
                                     B, T, N, K, heads, ACTS[act], _DT[x.dtype], wp, wn, st))
@@ -746,7 +746,7 @@ def linear_backward(x, w, dy, pre=None, act: str = "none", heads: int = 0, need=
     with _on(dev, stream) as st:
         dx = torch.empty_like(x) if need[0] else None
         dw = torch.empty_like(w) if need[1] else None
-        db = torch.empty((N,), dtype=torch.float32, device=dev) if need[2] else None
+        db = torch.empty(N, dtype=torch.float32, device=dev) if need[2] else None
         ws, wp, wn = _workspace(gecko_linear_workspace, (B, T, N, K, heads, ACTS[act], _DT[x.dtype], 1), dev)
         _check(gecko_linear_backward(x.data_ptr(), w.data_ptr(), dy.data_ptr(), _ptr(pre), _ptr(dx), _ptr(dw),
                                      _ptr(db), B, T, N, K, heads, ACTS[act], _DT[x.dtype], wp, wn, st))
