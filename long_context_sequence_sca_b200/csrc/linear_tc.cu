@@ -199,7 +199,7 @@ __device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// 16 consecutive values, of which the first 8 or all 16 are in the tensor.
+// 16 consecutive values.
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, bool wide) {
   uint32_t w[8];
 #pragma unroll
@@ -327,7 +327,7 @@ struct GemmCfg {
   static constexpr int kA = 128 * kBK * 2, kB = kBN / CG * kBK * 2, kStage = kA + kB;
   static constexpr int kStages = (232448 - 1024 - 512) / kStage > 8 ? 8 : (232448 - 1024 - 512) / kStage;
   static constexpr int kBarOff = kStages * kStage;
-  static constexpr int kNumBars = 2 * kStages + 4;   // full, empty; accumulator full, empty
+  static constexpr int kNumBars = 2 * kStages + 5;   // full, empty; accumulator full, empty; drain
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
   static constexpr uint32_t kTmemCols = 2 * kBN;
@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   uint64_t* empty = full + NS;
   uint64_t* acc_full = empty + NS;    // [2]
   uint64_t* acc_empty = acc_full + 2; // [2], used in the even CTA
+  uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kMiscOff + 4);
 
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
       mbar_init(acc_full + i, 1);
       mbar_init(acc_empty + i, kEpilogueWarps * CG);
     }
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -452,6 +454,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
           if (ok) umma_done<CG>(acc_full + acc);
         }
       }
+      if (!ok) {   // what was issued is done before TMEM is given back
+        umma_done<CG>(drain);
+        mbar_wait_drain(drain, 0);
+      }
     }
     __syncwarp();
   } else if (warp >= kEpilogueWarp) {
@@ -531,11 +537,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
 // Few rows (generation, short prompts) or few tiles: the product is bound by the
 // other operand's bytes, or by how long a tile takes, so the work is spread over
 // as many SMs as it reaches: tiles of 128 x FN, one per cluster, and the depth
-// shared by the cluster's CTAs, each with
-// a run of the k-blocks (balanced, none empty).  Their sums meet through
-// distributed shared memory: each CTA leaves its rows in the memory of its (now
-// idle) stages and takes an equal share of the columns, adding the CTAs' parts
-// in rank order.  One launch, and no working memory.
+// shared by the cluster's CTAs, each with a part of the k-blocks (balanced, none
+// empty).  Their sums meet through distributed shared memory: each CTA leaves its
+// rows in the memory of its (now idle) stages and takes an equal share of the
+// columns, adding the CTAs' parts in rank order.  One launch, and no working
+// memory.
 // What keeps the bytes coming is how many stages are on their way, so a stage
 // holds only the rows there are (to a multiple of 8): the MMA reads 128 all the
 // same, the others from the operand behind, and their results are not used.  (8 x

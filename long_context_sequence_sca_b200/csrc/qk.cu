@@ -331,7 +331,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
 // Each thread has its rows' pieces (z and the four output gradients) brought
 // into its own slots of a ring in shared memory, kStages rounds ahead.  (In
 // registers one round ahead was all there was room for beside the 64 running
-// sums: 49 us at 2 x 5003 x 16 x 64 against 33 us.)
+// sums: 43 us at 2 x 5003 x 16 x 64 against 33, now 31.)
 template <typename T, int D, int kRot>
 __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
   constexpr int S = kStages<T>, kParts = sizeof(T) / 2;   // 16-byte parts of a thread's 8 elements
