@@ -17,7 +17,7 @@
 // planes are added in ascending size.
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
-// ring of stages, one thread issues tcgen05.mma, eight warps empty the
+// ring of stages, one thread issues tcgen05.mma, eight or sixteen warps empty the
 // accumulator (TMEM, two of them in turn), a row per thread.
 // With CG = 2 a pair of CTAs shares one 256 x kBN tile: each loads its 128
 // rows of A and half the rows of B, so a k-block moves half the bytes per
@@ -143,15 +143,21 @@ __device__ __forceinline__ void tmem_give(uint32_t taddr, uint32_t cols) {
 
 constexpr int kBK = 64;              // k-block: one 128-byte swizzle row
 constexpr int kBN = 256;             // columns per tile
-constexpr int kGemmThreads = 384;    // TMA, MMA, TMEM, idle warp; eight epilogue warps
-constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8;
-constexpr int kBand = 32;            // columns an epilogue warp takes at a time
-constexpr int kBands = 256 / kBand / 2;   // bands of a tile per epilogue warp (two warps share a row quarter)
+constexpr int kEpilogueWarp = 4;     // after TMA, MMA, TMEM and an idle warp
+constexpr int kBand = 16;            // columns an epilogue warp takes at a time
+// Epilogue warps: each of the four row quarters of a tile has two where they hold
+// running sums (kSum), else four: what they wait for is each other's loads and
+// stores (4096 x 4096 x 512 with SiLU and residual: 39 us with eight warps, with
+// sixteen 35 us).
+template <bool kSum> constexpr int kEpilogueWarps = kSum ? 8 : 16;
+template <bool kSum> constexpr int kGemmThreads = 32 * (kEpilogueWarp + kEpilogueWarps<kSum>);
+constexpr int kFewThreads = 384;
 // Registers per thread after setmaxnreg: the running sums of 128 columns sit in
 // the epilogue warps'.  The split has to fit what the block was launched with
 // (setmaxnreg.inc would wait for more forever).
 constexpr int kRegsCtl = 56, kRegsEpilogue = 224;
-static_assert(128 * kRegsCtl + 256 * kRegsEpilogue <= kGemmThreads * 168, "setmaxnreg split above the launch registers");
+static_assert(128 * kRegsCtl + 256 * kRegsEpilogue <= kGemmThreads<true> * 168,
+              "setmaxnreg split above the launch registers");
 constexpr int kGroupM = 8;           // tiles of one column band done together (operand reuse in L2)
 
 struct GemmShape {
@@ -187,11 +193,11 @@ __device__ __forceinline__ Unit unit_at(const GemmShape& g, int u) {
 
 // -------------------------------------------------------------- epilogues --
 
-// A thread owns one row of the tile and takes 32 columns of it at a time, 16 by
-// 16, straight from registers to global memory: shared memory is busy feeding
-// the MMAs (a transpose through it took five times as long as the stores of
-// full 32-byte sectors that this makes).  `wide` says that rows and columns
-// of 16 are aligned for 32-byte accesses.
+// A thread owns one row of the tile and takes 16 columns of it at a time,
+// straight from registers to global memory: shared memory is busy feeding the
+// MMAs (a transpose through it took five times as long as the stores of full
+// 32-byte sectors that this makes).  `wide` says that rows and columns of 16 are
+// aligned for 32-byte accesses.
 
 __device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -226,8 +232,8 @@ __device__ __forceinline__ void store16(float* p, const float* v, bool wide) {
   }
 }
 
-// Forward: bias, activation, residual.  What has to be read for a band of 32
-// columns is fetched before the sums are waited for.
+// Forward: bias, activation, residual.  What has to be read for a band is
+// fetched before the sums are waited for.
 template <typename T>
 struct EpiForward {
   const float* bias;
@@ -236,16 +242,15 @@ struct EpiForward {
   float* pre;
   OutLayout lay;
   int act;
-  bool wide;       // of y (pre is fp32: rows of 8 are enough)
-  bool wide_pre;
+  bool wide, wide_pre;   // of y; of pre
   struct Fetched {
-    float bias[32];
-    Vec8<T> residual[4];
+    float bias[16];
+    Vec8<T> residual[2];
   };
   __device__ __forceinline__ int64_t row(int64_t m) const { return lay.row(m); }
   __device__ __forceinline__ void fetch(Fetched& f, int64_t row, int n, bool on) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const bool in = n + 8 * i < lay.N;
 #pragma unroll
       for (int j = 0; j < 8; ++j) f.bias[8 * i + j] = 0.f;
@@ -254,48 +259,49 @@ struct EpiForward {
     }
   }
   __device__ __forceinline__ void put(const Fetched& f, int64_t row, int n, int, float* v) const {
+    if (n >= lay.N) return;
+    const int64_t at[2] = {row + lay.col(n), row + lay.col(n + 8)};
+    const bool both = n + 8 < lay.N;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += f.bias[i];
+    for (int i = 0; i < 16; ++i) v[i] += f.bias[i];
+    if (pre) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (pre && n + 8 * i < lay.N) {
-        float* p = pre + row + lay.col(n + 8 * i);
-        uint32_t w[8];
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || both) {
+          float* p = pre + at[i];
+          uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
-        if (wide_pre) {
-          store_sector(p, w);
-        } else {
-          *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(p + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+          if (wide_pre) {
+            store_sector(p, w);
+          } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(p + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
-      }
     }
     if (act == kActSilu) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], kActSilu);
+      for (int i = 0; i < 16; ++i) v[i] = activate(v[i], kActSilu);
     } else if (act == kActGelu) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], kActGelu);
+      for (int i = 0; i < 16; ++i) v[i] = activate(v[i], kActGelu);
     }
+    if (residual) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (residual && n + 8 * i < lay.N) {
-        float r[8];
-        f.residual[i].get(r);
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || both) {
+          float r[8];
+          f.residual[i].get(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = n + 16 * i;
-      if (wide) {
-        if (c < lay.N) store16(y + row + lay.col(c), v + 16 * i, true);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (c + 8 * h < lay.N) store_f8(y + row + lay.col(c + 8 * h), *reinterpret_cast<float(*)[8]>(v + 16 * i + 8 * h));
-      }
+          for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
+        }
+    }
+    if (wide) {
+      store16(y + at[0], v, true);
+    } else {
+      store_f8(y + at[0], *reinterpret_cast<float(*)[8]>(v));
+      if (both) store_f8(y + at[1], *reinterpret_cast<float(*)[8]>(v + 8));
     }
   }
 };
@@ -312,11 +318,8 @@ struct EpiPlain {
   __device__ __forceinline__ void fetch(Fetched&, int64_t, int, bool) const {}
   __device__ __forceinline__ void put(const Fetched&, int64_t row, int n, int split, float* v) const {
     T* p = c + (int64_t)split * M * N + row + n;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (n + 16 * i + 8 < N) store16(p + 16 * i, v + 16 * i, wide);
-      else if (n + 16 * i < N) store_f8(p + 16 * i, *reinterpret_cast<float(*)[8]>(v + 16 * i));
-    }
+    if (n + 8 < N) store16(p, v, wide);
+    else if (n < N) store_f8(p, *reinterpret_cast<float(*)[8]>(v));
   }
 };
 
@@ -335,9 +338,9 @@ struct GemmCfg {
 };
 
 template <int CG, bool AMN, bool BMN, bool kSum, class Epi>
-__global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_constant__ CUtensorMap ma,
-                                                                  const __grid_constant__ CUtensorMap mb,
-                                                                  const GemmShape g, const Epi ep, int* status) {
+__global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __grid_constant__ CUtensorMap ma,
+                                                                        const __grid_constant__ CUtensorMap mb,
+                                                                        const GemmShape g, const Epi ep, int* status) {
   using Cfg = GemmCfg<CG>;
   constexpr int NS = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kEpilogueWarps * CG);
+      mbar_init(acc_empty + i, kEpilogueWarps<kSum> * CG);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -463,8 +466,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
   } else if (warp >= kEpilogueWarp) {
     if constexpr (kSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsEpilogue));
     // ----------------------------------------------------------- epilogue --
+    constexpr int kShare = kEpilogueWarps<kSum> / 4;         // warps per row quarter, taking bands in turn
+    constexpr int kBands = kBN / kBand / kShare;
     const int q = warp % 4;   // the TMEM lanes a warp may read: rows 32 q ..
-    const int first_band = (warp - kEpilogueWarp) / 4;   // two warps per row quarter take bands in turn
+    const int first_band = (warp - kEpilogueWarp) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + first_band * kBand;
     int k = 0;
     bool ok = true;
@@ -484,9 +489,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < kBands; ++j) {
-          float v[32];
-          tmem_ld32p(lanes + acc * kBN + 2 * j * kBand, reinterpret_cast<uint32_t*>(v));
-          if (j) ep.fetch(f, row, n0 + 2 * j * kBand, on);
+          float v[kBand];
+          tmem_ld16p(lanes + acc * kBN + j * kShare * kBand, reinterpret_cast<uint32_t*>(v));
+          if (j) ep.fetch(f, row, n0 + j * kShare * kBand, on);
           tmem_wait_ld();
           if (j == kBands - 1) {
             // the accumulator is read: the MMAs of the unit after next may write it
@@ -494,10 +499,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive_at(CG == 1 ? smem_u32(acc_empty + acc) : map_to(acc_empty + acc, 0));
           }
-          if (on) ep.put(f, row, n0 + 2 * j * kBand, t.split, v);
+          if (on) ep.put(f, row, n0 + j * kShare * kBand, t.split, v);
         }
       } else {
-        float sum[kBands][32] = {};
+        float sum[kBands][kBand] = {};
         const int runs = ((t.kb1 - t.kb0) * g.pairs + g.run - 1) / g.run;
         for (int r = 0; r < runs; ++r, ++k) {
           const int acc = k & 1;
@@ -505,12 +510,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < kBands; ++j) {
-            uint32_t v[32];
-            tmem_ld32p(lanes + acc * kBN + 2 * j * kBand, v);
+          for (int j = 0; j < kBands; j += 2) {
+            uint32_t v[2][kBand];
+            tmem_ld16p(lanes + acc * kBN + j * kShare * kBand, v[0]);
+            tmem_ld16p(lanes + acc * kBN + (j + 1) * kShare * kBand, v[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[j][i] += __uint_as_float(v[i]);
+            for (int i = 0; i < 2 * kBand; ++i) sum[j + i / kBand][i % kBand] += __uint_as_float(v[i / kBand][i % kBand]);
           }
           // the accumulator is read: the run after next may write it
           tc_fence_before();
@@ -521,8 +527,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_tc_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < kBands; ++j) {
           typename Epi::Fetched f;
-          ep.fetch(f, row, n0 + 2 * j * kBand, on);
-          if (on) ep.put(f, row, n0 + 2 * j * kBand, t.split, sum[j]);
+          ep.fetch(f, row, n0 + j * kShare * kBand, on);
+          if (on) ep.put(f, row, n0 + j * kShare * kBand, t.split, sum[j]);
         }
       }
     }
@@ -559,7 +565,7 @@ __host__ __device__ constexpr int few_rows(int64_t M, bool mn) {
 }
 
 template <int FN, bool AMN, bool BMN, class Epi>
-__global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
+__global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
                                                                    const __grid_constant__ CUtensorMap mb,
                                                                    const GemmShape g, const Epi ep, int* status) {
   const int a_bytes = few_rows(g.M, AMN) * kBK * 2, stage = a_bytes + FN * kBK * 2;
@@ -673,10 +679,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   cluster_sync();
   if (warp == 2) tmem_give<1>(tmem, FN);
   // this CTA's share of the columns, FN / S: four at a time from every CTA into its own rows (nobody
-  // else reads those), then bands of 32 through the epilogue
+  // else reads those), then bands of 16 through the epilogue
   float* own = reinterpret_cast<float*>(smem) + rank * (FN / S);
-  const int quads = FN / 4 / S, bands = FN / 32 / S;
-  for (int i = threadIdx.x; i < rows * quads && S > 1; i += kGemmThreads) {
+  const int quads = FN / 4 / S, bands = FN / kBand / S;
+  for (int i = threadIdx.x; i < rows * quads && S > 1; i += kFewThreads) {
     const int m = i / quads;
     float4* at = reinterpret_cast<float4*>(own + m * kFewPitch<FN>) + (i - m * quads);
     float4 w[4];
@@ -694,15 +700,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
     *at = v;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * bands; i += kGemmThreads) {
-    const int m = i / bands, c = (i - m * bands) * 32, n = n0 + rank * (FN / S) + c;
+  for (int i = threadIdx.x; i < rows * bands; i += kFewThreads) {
+    const int m = i / bands, c = (i - m * bands) * kBand, n = n0 + rank * (FN / S) + c;
     if (n >= g.N || *abort_flag) continue;
     typename Epi::Fetched f;
     const int64_t row = ep.row(m0 + m);
     ep.fetch(f, row, n, true);
-    float v[32];
+    float v[kBand];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
+    for (int j = 0; j < kBand; j += 4) {
       const float4 w = *reinterpret_cast<const float4*>(own + m * kFewPitch<FN> + c + j);
       v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
     }
@@ -711,26 +717,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_few_kernel(const __grid_
   cluster_sync();   // the others have read this CTA's memory
 }
 
-// Sum of the parts' sums, then the epilogue: a thread takes 32 columns of a row.
+// Sum of the parts' sums, then the epilogue: a thread takes 16 columns of a row.
 template <class Epi>
 __global__ void __launch_bounds__(128) gemm_sum_kernel(const float* part, int splits, int64_t M, int N, const Epi ep) {
-  const int bands = (N + 31) / 32;
+  const int bands = (N + kBand - 1) / kBand;
   const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (i >= M * bands) return;
   const int64_t m = i / bands;
-  const int n = (int)(i - m * bands) * 32;
-  float v[32];
+  const int n = (int)(i - m * bands) * kBand;
+  float v[kBand];
   typename Epi::Fetched f;
   const int64_t row = ep.row(m);
   ep.fetch(f, row, n, true);
   const float* p = part + m * N + n;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < 2; ++c)
     if (n + 8 * c < N) load_f8(p + 8 * c, *reinterpret_cast<float(*)[8]>(v + 8 * c));
   for (int s = 1; s < splits; ++s) {
     p += M * N;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c)
       if (n + 8 * c < N) {
         float w[8];
         load_f8(p + 8 * c, w);
@@ -853,12 +859,12 @@ EpiPlain<T> plain(void* c, int64_t M, int64_t N) {
 }
 
 template <class Kernel, class Epi>
-cudaError_t launch_gemm(Kernel kern, int ctas, int cluster, int smem, const CUtensorMap& ma, const CUtensorMap& mb,
-                        const GemmShape& g, const Epi& ep, int* status, cudaStream_t st) {
+cudaError_t launch_gemm(Kernel kern, int ctas, int threads, int cluster, int smem, const CUtensorMap& ma,
+                        const CUtensorMap& mb, const GemmShape& g, const Epi& ep, int* status, cudaStream_t st) {
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -879,10 +885,10 @@ cudaError_t run_gemm(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMa
     cudaFuncAttributes fa;
     return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
   }();
-  if (kSum && 128 * kRegsCtl + 256 * kRegsEpilogue > kGemmThreads * regs) return cudaErrorInvalidConfiguration;
+  if (kSum && 128 * kRegsCtl + 256 * kRegsEpilogue > kGemmThreads<true> * regs) return cudaErrorInvalidConfiguration;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits, slots = sm_count() / CG;
-  return launch_gemm(kern, (int)(CG * (units < slots ? units : slots)), CG, GemmCfg<CG>::kAlloc, ma, mb, g, ep, status,
-                     st);
+  return launch_gemm(kern, (int)(CG * (units < slots ? units : slots)), kGemmThreads<kSum>, CG, GemmCfg<CG>::kAlloc, ma,
+                     mb, g, ep, status, st);
 }
 
 // A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.
@@ -898,7 +904,7 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
   if ((e = BMN ? make_map(&mb, B, planes, K, N, kBK) : make_map(&mb, B, planes, N, K, b_rows))) return e;
   if (pl.cg == 0)
     return launch_gemm(pl.few_n == 128 ? gemm_few_kernel<128, AMN, BMN, Epi> : gemm_few_kernel<256, AMN, BMN, Epi>,
-                       pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, pl.g.splits, kFewAlloc, ma, mb, pl.g,
+                       pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, kFewThreads, pl.g.splits, kFewAlloc, ma, mb, pl.g,
                        ep, status, st);
   auto product = [&](const auto& out) -> cudaError_t {
     using Out = std::decay_t<decltype(out)>;
@@ -915,7 +921,8 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
   if (pl.g.splits == 1) return product(ep);
   float* part = static_cast<float*>(ws);
   if ((e = product(EpiPlain<float>{part, M, (int)N, aligned32(part)}))) return e;
-  gemm_sum_kernel<Epi><<<(unsigned)((M * ((N + 31) / 32) + 127) / 128), 128, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
+  gemm_sum_kernel<Epi>
+      <<<(unsigned)((M * ((N + kBand - 1) / kBand) + 127) / 128), 128, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
   return cudaGetLastError();
 }
 
