@@ -5,16 +5,16 @@
 //
 // fp32 operands come as three bf16 planes, v = h + m + l to 2^-25 of |v|, and
 // the product as the six plane products that reach 2^-24 (the other three are
-// below 2^-26): hh, hm, mh, mm, hl, lh.  To the kernel they are a product six
-// times as deep whose k-blocks come from different planes; at a sixth of the
-// bf16 rate this is still several times the rate of the fp32 FMA pipe.
+// below 2^-26): hh, hm, mh, mm, hl, lh.  To the large tiles' kernel they are a
+// product six times as deep whose k-blocks come from different planes; at a sixth
+// of the bf16 rate this is still several times the rate of the fp32 FMA pipe.
 //
 // The tensor core cuts its sums instead of rounding them, by about 2^-25.5 of
 // the sum a step (measured: 5e-6 of the result after 256 steps, which shows in
 // the fp32 results: y, pre, db).  Where it would (fp32, and bf16 with pre), a
 // product is cut into runs of 1024 (2048), whose sums the epilogue warps add up
 // in registers with rounding while the next run is under way (kSum), and the
-// planes are added in ascending size.
+// planes are added in ascending size, or apart from the first.
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
 // ring of stages, one thread issues tcgen05.mma, eight or sixteen warps empty the
@@ -552,6 +552,12 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
 // holds only the rows there are (to a multiple of 8): the MMA reads 128 all the
 // same, the others from the operand behind, and their results are not used.  (8 x
 // 4096 x 4096: 13.4 us with six whole stages, with eleven short ones 12.4.)
+// With kPlanes, a stage holds one plane of A and of B, loaded once for all of its
+// plane products (with a stage for each product, twice the bytes, 256 x 4096 x 1024
+// took 28.1 us against 25.7 and 64 x 4096 x 4096 70 against 58).  The order, middle
+// planes first, gives the stages back as they were taken.  The product of the
+// first planes has an accumulator to itself: as many of its sums are cut as of a
+// bf16 product's.
 constexpr int kFewRing = 196608, kFewMostStages = 12;   // bytes of the ring
 template <int FN> constexpr int kFewPitch = FN + 4;     // floats per row left in shared memory
 constexpr int kFewMiscOff = kFewRing + (2 * kFewMostStages + 1) * 8;
@@ -564,10 +570,11 @@ __host__ __device__ constexpr int few_rows(int64_t M, bool mn) {
   return mn || M > 120 ? 128 : (int)((M + 7) / 8 * 8);
 }
 
-template <int FN, bool AMN, bool BMN, class Epi>
+template <bool kPlanes, int FN, bool AMN, bool BMN, class Epi>
 __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
-                                                                   const __grid_constant__ CUtensorMap mb,
-                                                                   const GemmShape g, const Epi ep, int* status) {
+                                                                  const __grid_constant__ CUtensorMap mb,
+                                                                  const GemmShape g, const Epi ep, int* status) {
+  constexpr int kAcc = kPlanes ? 2 * FN : FN;   // TMEM columns: the first planes' product, behind it the others
   const int a_bytes = few_rows(g.M, AMN) * kBK * 2, stage = a_bytes + FN * kBK * 2;
   const int NS = min(kFewMostStages, kFewRing / stage);
   extern __shared__ uint8_t smem_raw[];
@@ -582,27 +589,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
   const int n0 = tile / g.tiles_m * FN, m0 = tile % g.tiles_m * 128;   // (tiles of one column band together)
   const int rows = (int)min((int64_t)128, g.M - m0);
   const int kb0 = g.k_blocks * rank / S, kb1 = g.k_blocks * (rank + 1) / S;
-  // one k-block of a plane product into a stage
-  auto load = [&](int s, int kb, int left) {
+  // load `it` into a stage: a k-block, or a plane of one (the middle one, the first, the last)
+  auto load = [&](int s, int it) {
     uint8_t *pa = smem + s * stage, *pb = pa + a_bytes;
     const uint32_t bar = smem_u32(full + s);
-    const int za = plane_a(left), zb = plane_b(left);
+    const int kb = kb0 + (kPlanes ? it / 3 : it), i3 = it % 3, z = !kPlanes || i3 == 1 ? 0 : i3 == 0 ? 1 : 2;
     mbar_arrive_expect_tx(full + s, stage);
     if (AMN) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) tma_load<1>(pa + i * 8192, &ma, bar, m0 + 64 * i, kb * kBK, za);
+      for (int i = 0; i < 2; ++i) tma_load<1>(pa + i * 8192, &ma, bar, m0 + 64 * i, kb * kBK, z);
     } else {
-      tma_load<1>(pa, &ma, bar, kb * kBK, m0, za);
+      tma_load<1>(pa, &ma, bar, kb * kBK, m0, z);
     }
     if (BMN) {
 #pragma unroll
-      for (int i = 0; i < FN / 64; ++i) tma_load<1>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK, zb);
+      for (int i = 0; i < FN / 64; ++i) tma_load<1>(pb + i * 8192, &mb, bar, n0 + 64 * i, kb * kBK, z);
     } else {
-      tma_load<1>(pb, &mb, bar, kb * kBK, n0, zb);
+      tma_load<1>(pb, &mb, bar, kb * kBK, n0, z);
     }
   };
-  const int blocks = (kb1 - kb0) * g.pairs;
-  int it = 0, kb = kb0, left = g.pairs - 1;   // the loading thread's place
+  const int blocks = (kb1 - kb0) * (kPlanes ? 3 : 1);
+  int it = 0;   // the loading thread's place
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
@@ -612,12 +619,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
     *abort_flag = 0;
     fence_mbar_init();
     // the first round of stages is on its way before anything else is set up
-    for (; it < NS && it < blocks; ++it) {
-      load(it, kb, left);
-      if (++kb == kb1) kb = kb0, --left;
-    }
+    for (; it < NS && it < blocks; ++it) load(it, it);
   }
-  if (warp == 2) tmem_take<1>(tmem_slot, FN);
+  if (warp == 2) tmem_take<1>(tmem_slot, kAcc);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -628,8 +632,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
       uint32_t phase = 0;   // of the wait for an emptied stage
       for (int s = 0; it < blocks; ++it) {
         if (!(ok = mbar_wait(empty + s, phase, abort_flag, status))) break;
-        load(s, kb, left);
-        if (++kb == kb1) kb = kb0, --left;
+        load(s, it);
         if (++s == NS) s = 0, phase ^= 1;
       }
       if (!ok)   // the copies issued land before the CTA exits
@@ -640,19 +643,52 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, FN, AMN, BMN);
       const uint32_t base = smem_u32(smem);
-      uint32_t phase = 0;
-      for (int it = 0, s = 0; it < blocks; ++it) {
-        if (!mbar_wait(full + s, phase, abort_flag, status)) break;
-        tc_fence_after();
-        const uint32_t a0 = base + s * stage, b0 = a0 + a_bytes;
+      auto product = [&](int sa, int sb, uint32_t acc, bool add) {
+        const uint32_t a0 = base + sa * stage, b0 = base + sb * stage + a_bytes;
         const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
         const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
-          umma<1>(tmem, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)), idesc,
-                  it > 0 || kk > 0 ? 1u : 0u);
-        umma_done<1>(empty + s);
+          umma<1>(acc, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)), idesc,
+                  add || kk > 0 ? 1u : 0u);
+      };
+      uint32_t phase = 0;
+      int s = 0;
+      auto arrived = [&] {
+        if (!mbar_wait(full + s, phase, abort_flag, status)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto next = [&] {
         if (++s == NS) s = 0, phase ^= 1;
+      };
+      if constexpr (!kPlanes) {
+        for (int it = 0; it < blocks; ++it, next()) {
+          if (!arrived()) break;
+          product(s, s, tmem, it > 0);
+          umma_done<1>(empty + s);
+        }
+      } else {
+        for (int it = 0; it < blocks; it += 3) {
+          const bool add = it > 0;
+          if (!arrived()) break;
+          const int mid = s;
+          product(mid, mid, tmem + FN, add);
+          next();
+          if (!arrived()) break;
+          const int first = s;
+          product(first, mid, tmem + FN, true);
+          product(mid, first, tmem + FN, true);
+          umma_done<1>(empty + mid);
+          product(first, first, tmem, add);
+          next();
+          if (!arrived()) break;
+          product(first, s, tmem + FN, true);
+          product(s, first, tmem + FN, true);
+          umma_done<1>(empty + first);
+          umma_done<1>(empty + s);
+          next();
+        }
       }
       umma_done<1>(acc_full);   // also after an abort: what was issued is done before TMEM is given back
       mbar_wait_drain(acc_full, 0);
@@ -666,7 +702,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
       for (int c = 0; c < FN / 2; c += 32) {
         uint32_t v[32];
         tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + half * (FN / 2) + c, v);
-        tmem_wait_ld();
+        if constexpr (kPlanes) {
+          uint32_t w[32];
+          tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + FN + half * (FN / 2) + c, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+        } else {
+          tmem_wait_ld();
+        }
         if (m < rows)
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
@@ -677,7 +721,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 2) tmem_give<1>(tmem, FN);
+  if (warp == 2) tmem_give<1>(tmem, kAcc);
   // this CTA's share of the columns, FN / S: four at a time from every CTA into its own rows (nobody
   // else reads those), then bands of 16 through the epilogue
   float* own = reinterpret_cast<float*>(smem) + rank * (FN / S);
@@ -825,9 +869,11 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   // Or the few-rows kernel's tiles, of 128 or 256 columns, whose clusters are to be
   // resident all at once (33 of 4 CTAs, 74 of 2: cudaOccupancyMaxActiveClusters; 16
   // of 8 where 15 fit took 20 us against 14).  The times in us that decide were
-  // fitted to 28 products from 8 x 4096 x 4096 to 3711 x 1000 x 1288, bf16 and
-  // fp32: 256 x 4096 x 4096 takes 20.5 with large tiles, 17.3 and 15.8 with these;
-  // 1024 x 1024 x 1024 12.2, 10.2 and 11.9; 1024 x 4096 x 4096 27.7, 27.3 and 31.2.
+  // fitted to 28 products from 8 x 4096 x 4096 to 3711 x 1000 x 1288: 256 x 4096 x
+  // 4096 takes 20.5 with large tiles, 17.3 and 15.8 with these; 1024 x 1024 x 1024
+  // 12.2, 10.2 and 11.9; 1024 x 4096 x 4096 27.7, 27.3 and 31.2.  For fp32 to 30 (with
+  // the splitting): 1024 x 1024 x 1024 takes 27.0, 22.0 and 23.7; 1024 x 1024 x 4096
+  // 64.1 and, in parts of a run, 56.8 with 256 columns.
   const int64_t waves = (t * g.splits + slots - 1) / slots;
   double best = (g.splits > 1 ? 14.0 + 0.5 * g.splits : 7.5) + 0.29 * g.blocks_per_split * g.pairs * waves;
   const int64_t k_blocks = g.k_blocks;
@@ -836,8 +882,9 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
     if (few_tiles > sm_count() && (M > 128 || n == 256)) continue;
     const int S = few_tiles <= 33 && k_blocks >= 8 ? 4 : few_tiles <= 74 && k_blocks >= 4 ? 2 : 1;
     if (exact && tiles(k_blocks, S) > g.run) continue;
-    const double work_part = (double)tiles(k_blocks, S) * g.pairs;
-    const double cost = n == 128 ? 6.3 + 0.325 * work_part : 9.0 + 0.36 * work_part;
+    const double part = tiles(k_blocks, S);
+    const double cost = planes == 3 ? (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
+                                    : (n == 128 ? 6.3 + 0.325 * part : 9.0 + 0.36 * part);
     if (cost > best && !(M <= 128 && pl.cg != 0)) continue;   // (one-CTA large tiles only where it must be)
     best = cost;
     pl.cg = 0;
@@ -891,10 +938,10 @@ cudaError_t run_gemm(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMa
                      mb, g, ep, status, st);
 }
 
-// A and B: bf16, or (planes 3) the bf16 planes of fp32 operands.
-template <bool AMN, bool BMN, bool kExact, class Epi>
-cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, int planes, const Epi& ep,
-                 void* ws, int* status, cudaStream_t st) {
+// A and B: bf16, or (planes = 3) the bf16 planes of fp32 operands.
+template <int planes, bool AMN, bool BMN, bool kExact, class Epi>
+cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, const Epi& ep, void* ws,
+                 int* status, cudaStream_t st) {
   const GemmPlan pl = gemm_plan(M, N, K, planes, kExact);
   CUtensorMap ma, mb;
   cudaError_t e;
@@ -903,7 +950,8 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
                : make_map(&ma, A, planes, M, K, pl.cg == 0 ? few_rows(M, false) : 128))) return e;
   if ((e = BMN ? make_map(&mb, B, planes, K, N, kBK) : make_map(&mb, B, planes, N, K, b_rows))) return e;
   if (pl.cg == 0)
-    return launch_gemm(pl.few_n == 128 ? gemm_few_kernel<128, AMN, BMN, Epi> : gemm_few_kernel<256, AMN, BMN, Epi>,
+    return launch_gemm(pl.few_n == 128 ? gemm_few_kernel<planes == 3, 128, AMN, BMN, Epi>
+                                       : gemm_few_kernel<planes == 3, 256, AMN, BMN, Epi>,
                        pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, kFewThreads, pl.g.splits, kFewAlloc, ma, mb, pl.g,
                        ep, status, st);
   auto product = [&](const auto& out) -> cudaError_t {
@@ -938,8 +986,9 @@ cudaError_t forward_tc(const LinearProblem& p, const void* xp, const void* wp, v
   const EpiForward<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act,
                          aligned32(p.y) && run % 16 == 0, aligned32(p.pre)};
   constexpr int planes = sizeof(T) == 4 ? 3 : 1;
-  if (planes == 3 || p.pre) return gemm<false, false, true>(p.M(), p.N, p.K, x, w, planes, ep, ws, p.status, st);
-  return gemm<false, false, false>(p.M(), p.N, p.K, x, w, planes, ep, ws, p.status, st);
+  if constexpr (planes == 1)
+    if (!p.pre) return gemm<1, false, false, false>(p.M(), p.N, p.K, x, w, ep, ws, p.status, st);
+  return gemm<planes, false, false, true>(p.M(), p.N, p.K, x, w, ep, ws, p.status, st);
 }
 
 }  // namespace
@@ -957,20 +1006,17 @@ cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* dup, int64_t
                                 cudaStream_t st) {
   const Operand du{dup, du_pitch}, w = operand(p, wp, p.K);
   if (p.dtype == kBF16)
-    return gemm<false, true, false>(p.M(), p.K, p.N, du, w, 1, plain<__nv_bfloat16>(p.dx, p.M(), p.K),
-                                    ws, p.status, st);
-  return gemm<false, true, true>(p.M(), p.K, p.N, du, w, 3, plain<float>(p.dx, p.M(), p.K), ws,
-                           p.status, st);
+    return gemm<1, false, true, false>(p.M(), p.K, p.N, du, w, plain<__nv_bfloat16>(p.dx, p.M(), p.K), ws, p.status,
+                                       st);
+  return gemm<3, false, true, true>(p.M(), p.K, p.N, du, w, plain<float>(p.dx, p.M(), p.K), ws, p.status, st);
 }
 
 cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* dup, int64_t du_pitch, const void* xp, void* ws,
                                 cudaStream_t st) {
   const Operand du{dup, du_pitch}, x = operand(p, xp, p.K);
   if (p.dtype == kBF16)
-    return gemm<true, true, false>(p.N, p.K, p.M(), du, x, 1, plain<__nv_bfloat16>(p.dw, p.N, p.K),
-                                   ws, p.status, st);
-  return gemm<true, true, true>(p.N, p.K, p.M(), du, x, 3, plain<float>(p.dw, p.N, p.K), ws,
-                          p.status, st);
+    return gemm<1, true, true, false>(p.N, p.K, p.M(), du, x, plain<__nv_bfloat16>(p.dw, p.N, p.K), ws, p.status, st);
+  return gemm<3, true, true, true>(p.N, p.K, p.M(), du, x, plain<float>(p.dw, p.N, p.K), ws, p.status, st);
 }
 
 }  // namespace gecko
