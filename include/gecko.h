@@ -354,7 +354,8 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
  * the call's work on its stream is done.  So calls on different streams, or
  * captured into different CUDA graphs, share nothing as long as they are given
  * different workspaces.  Every pointer is 16-byte aligned device memory of
- * the current device (reset: any alignment) and every tensor is contiguous.
+ * the current device (reset: any alignment; pos: 8 bytes) and every tensor is
+ * contiguous.
  * Outputs are fully overwritten and must not alias inputs or each other
  * except where stated.  Execution is asynchronous on `stream`; argument errors
  * are found on the host before anything is launched or written; a wait inside a
@@ -424,7 +425,7 @@ int gecko_gated_scan_backward(const void* x, const void* log_a, const void* dy, 
  *   pos          : [B, T] int64 positions, or NULL for pos0 + t.
  *   q, k, qm, km : [B, H, T, d] dtype.
  *   Requires d in {64, 128}, rot_dim a multiple of 16 with 0 <= rot_dim <= d,
- *   rot_base >= 1 (read if rot_dim > 0), eps > 0, H <= 65535,
+ *   rot_base >= 1 (read if rot_dim > 0), eps >= 2^-60, H <= 65535,
  *   B, T < 2^31, B * T < 2^35.
  *
  * gecko_qk_backward - its gradients for dq, dk, dqm, dkm [B, H, T, d]:

@@ -113,7 +113,8 @@ int check_qk_sizes(int64_t B, int64_t T, int64_t H, int64_t d, float eps, int64_
   if (int rc = check_dtype(dtype)) return rc;
   if (B < 1 || T < 1 || H < 1)
     return fail(GECKO_ERR_ARG, "sizes must be >= 1 (B=%lld T=%lld H=%lld)", (long long)B, (long long)T, (long long)H);
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(GECKO_ERR_ARG, "eps must be positive and finite");
+  // (below 2^-60, rows longer than eps could have squares that vanish in fp32)
+  if (!(eps >= 0x1p-60f) || !std::isfinite(eps)) return fail(GECKO_ERR_ARG, "eps must be at least 2^-60 and finite");
   if (rot_dim < 0) return fail(GECKO_ERR_ARG, "rot_dim must be >= 0");
   if (rot_dim > 0 && (!(rot_base >= 1.0) || !std::isfinite(rot_base)))
     return fail(GECKO_ERR_ARG, "rot_base must be finite and at least 1");
@@ -125,6 +126,11 @@ int check_qk_sizes(int64_t B, int64_t T, int64_t H, int64_t d, float eps, int64_
     return fail(GECKO_ERR_SHAPE, "B, T or H exceeds the kernels' range (B=%lld T=%lld H=%lld)", (long long)B,
                 (long long)T, (long long)H);
   return GECKO_OK;
+}
+
+// (read one at a time: a token's slice of a row of positions will do)
+int check_positions(const int64_t* pos) {
+  return reinterpret_cast<uintptr_t>(pos) % 8 ? fail(GECKO_ERR_ALIGN, "pos is not 8-byte aligned") : GECKO_OK;
 }
 
 void set_rotation(QkProblem& p, int64_t rot_dim, double rot_base, int interleaved) {
@@ -139,7 +145,7 @@ int qk_forward(const void* z, const float* scale, const float* shift, const int6
                double rot_base, int interleaved, int dtype, void* stream) {
   int rc;
   if ((rc = check_qk_sizes(B, T, H, d, eps, rot_dim, rot_base, dtype))) return rc;
-  if ((rc = check_pointers({z, scale, shift, q, k, qm, km}, {pos}))) return rc;
+  if ((rc = check_pointers({z, scale, shift, q, k, qm, km}, {})) || (rc = check_positions(pos))) return rc;
   QkProblem p{};
   p.z = z, p.scale = scale, p.shift = shift, p.pos = pos;
   p.out[0] = q, p.out[1] = k, p.out[2] = qm, p.out[3] = km;
@@ -155,7 +161,8 @@ int qk_backward(const void* z, const float* scale, const int64_t* pos, const voi
                 int dtype, void* ws, int64_t ws_bytes, void* stream) {
   int rc;
   if ((rc = check_qk_sizes(B, T, H, d, eps, rot_dim, rot_base, dtype))) return rc;
-  if ((rc = check_pointers({z, scale, dq, dk, dqm, dkm, dz, dscale, dshift}, {pos}))) return rc;
+  if ((rc = check_pointers({z, scale, dq, dk, dqm, dkm, dz, dscale, dshift}, {})) || (rc = check_positions(pos)))
+    return rc;
   if ((rc = check_workspace(ws, ws_bytes, qk_workspace_bytes(B, T, H, d)))) return rc;
   QkProblem p{};
   p.z = z, p.scale = scale, p.pos = pos;

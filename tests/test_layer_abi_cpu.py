@@ -64,13 +64,13 @@ def _qk_bwd(at={}, B=1, T=10, H=2, d=64, eps=1e-6, pos0=0, rot=64, base=10000.0,
                                ws, n, None)
 
 
-QK = [(dict(B=0), 1), (dict(T=0), 1), (dict(H=0), 1), (dict(dtype=9), 1), (dict(eps=0.0), 1),
+QK = [(dict(B=0), 1), (dict(T=0), 1), (dict(H=0), 1), (dict(dtype=9), 1), (dict(eps=0.0), 1), (dict(eps=1e-20), 1),
       (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(rot=-16), 1), (dict(base=0.5), 1),
       (dict(base=float("inf")), 1), (dict(d=96), 2), (dict(rot=24), 2), (dict(rot=80), 2), (dict(H=65536), 2),
       (dict(B=1 << 31), 2), (dict(B=1 << 18, T=1 << 18), 2)]
 
 
-@pytest.mark.parametrize("kw,code", QK + [(dict(at={0: 0}), 1), (dict(at={7: 0}), 1), (dict(at={3: FAKE + 8}), 3),
+@pytest.mark.parametrize("kw,code", QK + [(dict(at={0: 0}), 1), (dict(at={7: 0}), 1), (dict(at={3: FAKE + 4}), 3),
                                           (dict(at={5: FAKE + 4}), 3)])
 def test_qk_rejects(so, kw, code):
     assert _qk(**kw) == code and L.gecko_last_error()

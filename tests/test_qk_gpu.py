@@ -111,6 +111,15 @@ def test_far_and_given_positions(L, inter, dtype):
     check(L, _inputs(1, 9, 2, 64, dtype, seed=5), dtype, 32, inter, pos0=-7, base=500000.0)
 
 
+def test_one_token_of_a_row_of_positions(L):
+    """A generated token's position as a slice of its sequence's: 8-byte aligned."""
+    inp = _inputs(1, 1, 4, 64, "bf16", seed=8)
+    row = torch.arange(100, 110, device="cuda")[None]
+    for t in (4, 5):
+        inp["pos"] = row[:, t:t + 1]
+        check(L, inp, "bf16", 64)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_zero_and_tiny_rows(L, dtype):
     """A row of zeros gives z' = 0, rows shorter than eps a linear map."""
