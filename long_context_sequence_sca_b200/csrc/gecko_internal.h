@@ -298,10 +298,11 @@ inline int64_t plane_pitch(int64_t inner) { return (inner + 63) / 64 * 64; }
 // three bf16 planes for fp32.  ws: gemm_tc_workspace of the product's rows,
 // columns and depth.
 size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype);
-cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st);
+cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, bool after,
+                             cudaStream_t st);
 cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* du, int64_t du_pitch, const void* w, void* ws,
-                                cudaStream_t st);
+                                bool after, cudaStream_t st);
 cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* du, int64_t du_pitch, const void* x, void* ws,
-                                cudaStream_t st);
+                                bool after, cudaStream_t st);
 
 }  // namespace gecko

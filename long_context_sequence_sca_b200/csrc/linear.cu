@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
                                                                    OutLayout lay, int64_t M, int64_t N, int64_t rows,
                                                                    int64_t pitch) {
   __shared__ float red[kDuRowsPar][kDuCols];
+  let_next_start();
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int64_t n = (int64_t)blockIdx.x * kDuCols + cx * 8;
   const int64_t m1 = min(M, ((int64_t)blockIdx.y + 1) * rows);
@@ -242,6 +243,8 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
 // db: the partial column sums in a fixed order.
 __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int rows, int64_t N, float* db) {
   __shared__ float red[8][32];
+  let_next_start();
+  wait_for_previous();
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + cx;
   float acc = 0.f;
@@ -293,6 +296,8 @@ struct SplitArgs {
   int64_t pitch;
 };
 __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
+  let_next_start();
+  wait_for_previous();
   const uint32_t per_row = a.inner / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   int64_t r = i / per_row;
@@ -305,14 +310,15 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
   store_planes(a.planes[which] + r * a.pitch + c, a.rows[which] * a.pitch, w);
 }
 
-void launch_split(const void* v0, void* p0, int64_t rows0, const void* v1, void* p1, int64_t rows1, int64_t inner,
-                  cudaStream_t st) {
+cudaError_t launch_split(const void* v0, void* p0, int64_t rows0, const void* v1, void* p1, int64_t rows1,
+                         int64_t inner, bool after, cudaStream_t st) {
   const SplitArgs a{{static_cast<const float*>(v0), static_cast<const float*>(v1)},
                     {static_cast<__nv_bfloat16*>(p0), static_cast<__nv_bfloat16*>(p1)},
                     {rows0, rows1},
                     (uint32_t)inner,
                     plane_pitch(inner)};
-  split_kernel<<<(unsigned)(((rows0 + rows1) * (inner / 8) + 255) / 256), 256, 0, st>>>(a);
+  return launch_chained(split_kernel, dim3((unsigned)(((rows0 + rows1) * (inner / 8) + 255) / 256)), 256, 0, 0, after,
+                        st, a);
 }
 
 // GECKO_KERNELS=simt selects the CUDA-core kernels for every type.
@@ -375,9 +381,9 @@ cudaError_t forward_impl(const LinearProblem& p, cudaStream_t st) {
   }
   const Layout l = layout_of(p, false);
   char* ws = static_cast<char*>(p.ws);
-  if (p.dtype == kBF16) return launch_linear_tc(p, p.x, p.w, ws + l.gemm, st);
-  launch_split(p.x, ws + l.x, p.M(), p.w, ws + l.w, p.N, p.K, st);
-  return launch_linear_tc(p, ws + l.x, ws + l.w, ws + l.gemm, st);
+  if (p.dtype == kBF16) return launch_linear_tc(p, p.x, p.w, ws + l.gemm, false, st);
+  if (cudaError_t e = launch_split(p.x, ws + l.x, p.M(), p.w, ws + l.w, p.N, p.K, false, st)) return e;
+  return launch_linear_tc(p, ws + l.x, ws + l.w, ws + l.gemm, true, st);
 }
 
 template <typename T>
@@ -390,13 +396,19 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   const bool tc = use_tc(), products = p.dx || p.dw;
   const bool alias = tc ? l.dy_is_du : p.act == kActNone && p.H == 0;
   const int64_t pitch = tc && !alias ? plane_pitch(p.N) : p.N;   // of du
+  bool after = false;
+  cudaError_t e;
   if (p.db || (!alias && products)) {
     const int64_t blocks = du_row_blocks(M, p.N);
     void* du = products && !alias ? ws + l.du : nullptr;
     float* sums = !p.db ? nullptr : blocks == 1 ? p.db : part;   // one block of rows: its sums are db
     if (tc && f32) launch_du<T, true>(p, du, pitch, sums, blocks, st);
     else launch_du<T, false>(p, du, pitch, sums, blocks, st);
-    if (p.db && blocks > 1) linear_db_kernel<<<(unsigned)((p.N + 31) / 32), 256, 0, st>>>(part, (int)blocks, p.N, p.db);
+    after = true;
+    if (p.db && blocks > 1 &&
+        (e = launch_chained(linear_db_kernel, dim3((unsigned)((p.N + 31) / 32)), 256, 0, 0, after, st, part, (int)blocks,
+                            p.N, p.db)))
+      return e;
   }
   const void* g = alias ? p.dy : ws + l.du;
   if (!tc) {
@@ -406,13 +418,13 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
   }
   const void *x = p.x, *w = p.w;
   if (f32 && products) {
-    launch_split(p.x, ws + l.x, p.dw ? M : 0, p.w, ws + l.w, p.dx ? p.N : 0, p.K, st);
+    if ((e = launch_split(p.x, ws + l.x, p.dw ? M : 0, p.w, ws + l.w, p.dx ? p.N : 0, p.K, after, st))) return e;
+    after = true;
     x = ws + l.x;
     w = ws + l.w;
   }
-  cudaError_t e;
-  if (p.dx && (e = launch_linear_dx_tc(p, g, pitch, w, ws + l.gemm, st))) return e;
-  if (p.dw && (e = launch_linear_dw_tc(p, g, pitch, x, ws + l.gemm, st))) return e;
+  if (p.dx && (e = launch_linear_dx_tc(p, g, pitch, w, ws + l.gemm, after, st))) return e;
+  if (p.dw && (e = launch_linear_dw_tc(p, g, pitch, x, ws + l.gemm, after || p.dx, st))) return e;
   return cudaGetLastError();
 }
 

@@ -2,6 +2,7 @@
 // loads and stores, and the output layouts.
 #pragma once
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "gecko_internal.h"
 

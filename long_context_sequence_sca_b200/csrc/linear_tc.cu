@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
   const uint32_t rank = CG == 1 ? 0 : cluster_rank();
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   const int units = g.tiles_m * g.tiles_n * g.splits;
+  let_next_start();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -376,6 +377,7 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
     tma_prefetch_desc(&mb);
   }
   if (warp == 2) tmem_take<CG>(tmem_slot, Cfg::kTmemCols);
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();
@@ -610,6 +612,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
   };
   const int blocks = (kb1 - kb0) * (kPlanes ? 3 : 1);
   int it = 0;   // the loading thread's place
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
@@ -618,10 +621,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
     mbar_init(acc_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    wait_for_previous();
     // the first round of stages is on its way before anything else is set up
     for (; it < NS && it < blocks; ++it) load(it, it);
   }
   if (warp == 2) tmem_take<1>(tmem_slot, kAcc);
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -764,6 +769,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
 // Sum of the parts' sums, then the epilogue: a thread takes 16 columns of a row.
 template <class Epi>
 __global__ void __launch_bounds__(128) gemm_sum_kernel(const float* part, int splits, int64_t M, int N, const Epi ep) {
+  let_next_start();
+  wait_for_previous();
   const int bands = (N + kBand - 1) / kBand;
   const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (i >= M * bands) return;
@@ -907,25 +914,15 @@ EpiPlain<T> plain(void* c, int64_t M, int64_t N) {
 
 template <class Kernel, class Epi>
 cudaError_t launch_gemm(Kernel kern, int ctas, int threads, int cluster, int smem, const CUtensorMap& ma,
-                        const CUtensorMap& mb, const GemmShape& g, const Epi& ep, int* status, cudaStream_t st) {
+                        const CUtensorMap& mb, const GemmShape& g, const Epi& ep, int* status, bool after,
+                        cudaStream_t st) {
   if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g, ep, status);
+  return launch_chained(kern, dim3((unsigned)ctas), threads, smem, cluster, after, st, ma, mb, g, ep, status);
 }
 
 template <int CG, bool AMN, bool BMN, bool kSum, class Epi>
 cudaError_t run_gemm(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& ep, int* status,
-                     cudaStream_t st) {
+                     bool after, cudaStream_t st) {
   const GemmShape& g = pl.g;
   auto kern = gemm_tc_kernel<CG, AMN, BMN, kSum, Epi>;
   static const int regs = [&] {
@@ -935,13 +932,13 @@ cudaError_t run_gemm(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMa
   if (kSum && 128 * kRegsCtl + 256 * kRegsEpilogue > kGemmThreads<true> * regs) return cudaErrorInvalidConfiguration;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits, slots = sm_count() / CG;
   return launch_gemm(kern, (int)(CG * (units < slots ? units : slots)), kGemmThreads<kSum>, CG, GemmCfg<CG>::kAlloc, ma,
-                     mb, g, ep, status, st);
+                     mb, g, ep, status, after, st);
 }
 
 // A and B: bf16, or (planes = 3) the bf16 planes of fp32 operands.
 template <int planes, bool AMN, bool BMN, bool kExact, class Epi>
 cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operand& B, const Epi& ep, void* ws,
-                 int* status, cudaStream_t st) {
+                 int* status, bool after, cudaStream_t st) {
   const GemmPlan pl = gemm_plan(M, N, K, planes, kExact);
   CUtensorMap ma, mb;
   cudaError_t e;
@@ -953,25 +950,24 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
     return launch_gemm(pl.few_n == 128 ? gemm_few_kernel<planes == 3, 128, AMN, BMN, Epi>
                                        : gemm_few_kernel<planes == 3, 256, AMN, BMN, Epi>,
                        pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, kFewThreads, pl.g.splits, kFewAlloc, ma, mb, pl.g,
-                       ep, status, st);
+                       ep, status, after, st);
   auto product = [&](const auto& out) -> cudaError_t {
     using Out = std::decay_t<decltype(out)>;
     if constexpr (kExact) {
       if (pl.sum)
-        return pl.cg == 2 ? run_gemm<2, AMN, BMN, true, Out>(pl, ma, mb, out, status, st)
-                          : run_gemm<1, AMN, BMN, true, Out>(pl, ma, mb, out, status, st);
+        return pl.cg == 2 ? run_gemm<2, AMN, BMN, true, Out>(pl, ma, mb, out, status, after, st)
+                          : run_gemm<1, AMN, BMN, true, Out>(pl, ma, mb, out, status, after, st);
       // (one CTA per tile: only where the few-rows kernel would not be exact)
-      if (pl.cg == 1) return run_gemm<1, AMN, BMN, false, Out>(pl, ma, mb, out, status, st);
+      if (pl.cg == 1) return run_gemm<1, AMN, BMN, false, Out>(pl, ma, mb, out, status, after, st);
     }
     if (pl.cg != 2) return cudaErrorInvalidValue;   // (the maps are made for pl.cg)
-    return run_gemm<2, AMN, BMN, false, Out>(pl, ma, mb, out, status, st);
+    return run_gemm<2, AMN, BMN, false, Out>(pl, ma, mb, out, status, after, st);
   };
   if (pl.g.splits == 1) return product(ep);
   float* part = static_cast<float*>(ws);
   if ((e = product(EpiPlain<float>{part, M, (int)N, aligned32(part)}))) return e;
-  gemm_sum_kernel<Epi>
-      <<<(unsigned)((M * ((N + kBand - 1) / kBand) + 127) / 128), 128, 0, st>>>(part, pl.g.splits, M, (int)N, ep);
-  return cudaGetLastError();
+  return launch_chained(gemm_sum_kernel<Epi>, dim3((unsigned)((M * ((N + kBand - 1) / kBand) + 127) / 128)), 128, 0, 0,
+                        true, st, part, pl.g.splits, M, (int)N, ep);
 }
 
 // x or w: rows of the tensor, or of its planes.
@@ -980,15 +976,15 @@ Operand operand(const LinearProblem& p, const void* at, int64_t inner) {
 }
 
 template <typename T>
-cudaError_t forward_tc(const LinearProblem& p, const void* xp, const void* wp, void* ws, cudaStream_t st) {
+cudaError_t forward_tc(const LinearProblem& p, const void* xp, const void* wp, void* ws, bool after, cudaStream_t st) {
   const Operand x = operand(p, xp, p.K), w = operand(p, wp, p.K);
   const int64_t run = p.H ? p.N / p.H : p.N;   // contiguous columns
   const EpiForward<T> ep{p.bias, static_cast<const T*>(p.residual), static_cast<T*>(p.y), p.pre, OutLayout(p), p.act,
                          aligned32(p.y) && run % 16 == 0, aligned32(p.pre)};
   constexpr int planes = sizeof(T) == 4 ? 3 : 1;
   if constexpr (planes == 1)
-    if (!p.pre) return gemm<1, false, false, false>(p.M(), p.N, p.K, x, w, ep, ws, p.status, st);
-  return gemm<planes, false, false, true>(p.M(), p.N, p.K, x, w, ep, ws, p.status, st);
+    if (!p.pre) return gemm<1, false, false, false>(p.M(), p.N, p.K, x, w, ep, ws, p.status, after, st);
+  return gemm<planes, false, false, true>(p.M(), p.N, p.K, x, w, ep, ws, p.status, after, st);
 }
 
 }  // namespace
@@ -998,25 +994,28 @@ size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
   return pl.cg == 0 || pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
 }
 
-cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, cudaStream_t st) {
-  return p.dtype == kBF16 ? forward_tc<__nv_bfloat16>(p, x, w, ws, st) : forward_tc<float>(p, x, w, ws, st);
+cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, bool after,
+                             cudaStream_t st) {
+  return p.dtype == kBF16 ? forward_tc<__nv_bfloat16>(p, x, w, ws, after, st)
+                          : forward_tc<float>(p, x, w, ws, after, st);
 }
 
 cudaError_t launch_linear_dx_tc(const LinearProblem& p, const void* dup, int64_t du_pitch, const void* wp, void* ws,
-                                cudaStream_t st) {
+                                bool after, cudaStream_t st) {
   const Operand du{dup, du_pitch}, w = operand(p, wp, p.K);
   if (p.dtype == kBF16)
     return gemm<1, false, true, false>(p.M(), p.K, p.N, du, w, plain<__nv_bfloat16>(p.dx, p.M(), p.K), ws, p.status,
-                                       st);
-  return gemm<3, false, true, true>(p.M(), p.K, p.N, du, w, plain<float>(p.dx, p.M(), p.K), ws, p.status, st);
+                                       after, st);
+  return gemm<3, false, true, true>(p.M(), p.K, p.N, du, w, plain<float>(p.dx, p.M(), p.K), ws, p.status, after, st);
 }
 
 cudaError_t launch_linear_dw_tc(const LinearProblem& p, const void* dup, int64_t du_pitch, const void* xp, void* ws,
-                                cudaStream_t st) {
+                                bool after, cudaStream_t st) {
   const Operand du{dup, du_pitch}, x = operand(p, xp, p.K);
   if (p.dtype == kBF16)
-    return gemm<1, true, true, false>(p.N, p.K, p.M(), du, x, plain<__nv_bfloat16>(p.dw, p.N, p.K), ws, p.status, st);
-  return gemm<3, true, true, true>(p.N, p.K, p.M(), du, x, plain<float>(p.dw, p.N, p.K), ws, p.status, st);
+    return gemm<1, true, true, false>(p.N, p.K, p.M(), du, x, plain<__nv_bfloat16>(p.dw, p.N, p.K), ws, p.status,
+                                      after, st);
+  return gemm<3, true, true, true>(p.N, p.K, p.M(), du, x, plain<float>(p.dw, p.N, p.K), ws, p.status, after, st);
 }
 
 }  // namespace gecko

@@ -8,6 +8,7 @@
 // Everything is held in fp32; the angles are formed in revolutions in fp64
 // (a position of some millions times a rate has no bits left below one
 // revolution in fp32) and reduced to [-1/2, 1/2] before the fp32 sincospi.
+#include "chain.cuh"
 #include "common.cuh"
 #include "gecko_internal.h"
 
@@ -335,6 +336,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
 template <typename T, int D, int kRot>
 __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
   constexpr int S = kStages<T>, kParts = sizeof(T) / 2;   // 16-byte parts of a thread's 8 elements
+  let_next_start();
   extern __shared__ uint4 smem[];
   uint4* ring = smem;                                          // [S][5][kParts][threads]
   float4* turns = reinterpret_cast<float4*>(smem + S * 5 * kParts * kBwdThreads);
@@ -482,6 +484,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const _
 __global__ void __launch_bounds__(256) qk_bwd_sum_kernel(const float* part, int rows, int64_t cols, float* dscale,
                                                          float* dshift) {
   __shared__ float red[8][32];
+  wait_for_previous();
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + cx;
   float acc = 0.f;
@@ -597,9 +600,8 @@ cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st) {
   const Plan pl = bwd_plan(p.B, p.T, p.H, p.d);
   if (cudaError_t e = run(p, pl, true, st)) return e;
   const int64_t cols = 4 * p.H * p.d;
-  qk_bwd_sum_kernel<<<(unsigned)(2 * cols / 32), 256, 0, st>>>(static_cast<const float*>(p.ws), (int)pl.token_blocks,
-                                                               cols, p.dscale, p.dshift);
-  return cudaGetLastError();
+  return launch_chained(qk_bwd_sum_kernel, dim3((unsigned)(2 * cols / 32)), 256, 0, 0, true, st,
+                        static_cast<const float*>(p.ws), (int)pl.token_blocks, cols, p.dscale, p.dshift);
 }
 
 }  // namespace gecko

@@ -22,6 +22,7 @@
 // chunks, and the association, and with it every bit of the result, does not
 // depend on timing.  What is published is its own flag: the memory starts as
 // all ones, a pattern that no result has.
+#include "chain.cuh"
 #include "common.cuh"
 #include "gecko_internal.h"
 
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 6) scan_kernel(const __grid_constant
     mbar_init(&sm.bar, 1);
     fence_mbar_init();
   }
+  wait_for_previous();   // the hand-off's memory is set
   const Tile t = draw_tile(a, &sm.unit);
   const int64_t t0 = (int64_t)t.c * kScanChunk;
   if (threadIdx.x == 0) {
@@ -611,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_bwd_kernel(const __grid_cons
     mbar_init(&sm.bar, 1);
     fence_mbar_init();
   }
+  wait_for_previous();   // the hand-off's memory is set
   const Tile t = draw_tile(a, &sm.unit);
   const int c = a.C - 1 - t.c;
   const int64_t t0 = (int64_t)c * kScanChunk;
@@ -727,11 +730,20 @@ int64_t tiles_of(int64_t D, int dtype) {
 constexpr size_t kSyncBytes = 256;
 int64_t groups_of(int64_t L) { return (scan_chunks(L) + kGroup - 1) / kGroup; }
 
+// All ones over the hand-off's memory.
+__global__ void __launch_bounds__(256) scan_clear_kernel(uint4* p, int64_t n) {
+  let_next_start();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
 // Fill the arguments, enter and leave being the states at the walk's ends, and
 // set the hand-off's memory to all ones.  The last chunk may be done before others of the
 // first group have read the entering state, so if it is to be overwritten
-// they read a copy (in the slot of the first group's state).
-cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, ScanArgs* a, cudaStream_t st) {
+// they read a copy (in the slot of the first group's state).  *chained: the
+// scan may be launched as the clearing kernel's next.
+cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, ScanArgs* a, bool* chained,
+                     cudaStream_t st) {
   a->reset = p.reset;
   a->chunk_state = p.chunk_state;
   a->L = p.L;
@@ -748,8 +760,12 @@ cudaError_t set_args(const ScanProblem& p, const float* enter, float* leave, Sca
   a->enter0 = enter;
   a->enter0_stride = p.D;
   a->leave = leave;
+  *chained = a->C > 1 && !(enter && enter == leave);
   if (a->C == 1) return cudaSuccess;
-  if (cudaError_t e = cudaMemsetAsync(ws, 0xff, scan_workspace_bytes(p.B, p.L, p.D, p.dtype, false), st)) return e;
+  const int64_t words = (int64_t)scan_workspace_bytes(p.B, p.L, p.D, p.dtype, false) / 16, blocks = (words + 255) / 256;
+  const int64_t wave = 4 * (int64_t)sm_count();
+  scan_clear_kernel<<<(unsigned)(blocks < wave ? blocks : wave), 256, 0, st>>>(reinterpret_cast<uint4*>(ws), words);
+  if (cudaError_t e = cudaGetLastError()) return e;
   if (enter && enter == leave) {
     a->enter0 = reinterpret_cast<float*>(a->group);
     a->enter0_stride = groups_of(p.L) * p.D;
@@ -778,12 +794,13 @@ cudaError_t scan_impl(const ScanProblem& p, cudaStream_t st) {
   if (!make_map<T>(&mx, p.x, p) || !make_map<T>(&mg, p.log_a, p) || !make_map<T>(&my, p.y, p))
     return cudaErrorInvalidValue;
   ScanArgs a;
+  bool chained;
   cudaError_t e;
-  if ((e = set_args(p, p.state_in, p.state_out, &a, st))) return e;
+  if ((e = set_args(p, p.state_in, p.state_out, &a, &chained, st))) return e;
   constexpr int smem = 2 * kTileBytes + 128;
   if ((e = cudaFuncSetAttribute(scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-  scan_kernel<T><<<(unsigned)(a.C * a.B * a.tiles), kThreads, smem, st>>>(mx, mg, my, a);
-  return cudaGetLastError();
+  return launch_chained(scan_kernel<T>, dim3((unsigned)(a.C * a.B * a.tiles)), kThreads, smem, 0, chained, st, mx, mg, my,
+                        a);
 }
 
 template <typename T>
@@ -793,12 +810,13 @@ cudaError_t scan_bwd_impl(const ScanProblem& p, cudaStream_t st) {
       !make_map<T>(&mdx, p.dx, p) || !make_map<T>(&mdg, p.dlog_a, p))
     return cudaErrorInvalidValue;
   ScanArgs a;
+  bool chained;
   cudaError_t e;
-  if ((e = set_args(p, p.dstate_out, p.dstate_in, &a, st))) return e;
+  if ((e = set_args(p, p.dstate_out, p.dstate_in, &a, &chained, st))) return e;
   constexpr int smem = 3 * kTileBytes + 128;
   if ((e = cudaFuncSetAttribute(scan_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-  scan_bwd_kernel<T><<<(unsigned)(a.C * a.B * a.tiles), kThreads, smem, st>>>(mx, mg, mdy, mdx, mdg, a);
-  return cudaGetLastError();
+  return launch_chained(scan_bwd_kernel<T>, dim3((unsigned)(a.C * a.B * a.tiles)), kThreads, smem, 0, chained, st, mx,
+                        mg, mdy, mdx, mdg, a);
 }
 
 }  // namespace
