@@ -41,6 +41,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of it, for work between that needs nothing of the other CTAs.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Shared-memory address of `p` in the CTA of rank `rank`.
 __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
   uint32_t r;
@@ -105,6 +110,17 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True for one thread of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
 
 // Arrive on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
@@ -431,7 +447,8 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
     __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer --
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {   // (the whole warp walks the loop: see gemm_few_kernel)
+      const bool leader = elect_one();
       constexpr uint32_t idesc = idesc_bf16_f32(128 * CG, kBN, AMN, BMN);
       const uint32_t base = smem_u32(smem);
       int it = 0, k = 0;
@@ -441,26 +458,30 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
         const int blocks = (t.kb1 - t.kb0) * g.pairs;
         for (int kb = 0; kb < blocks && ok; ++k) {   // k counts runs
           const int acc = k & 1, end = kSum ? min(kb + g.run, blocks) : blocks;
-          if (k >= 2 && !(ok = mbar_wait_cluster(acc_empty + acc, (k / 2 - 1) & 1, abort_flag, status))) break;
+          if (k >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_empty + acc, (k / 2 - 1) & 1, abort_flag,
+                                                                        status))))
+            break;
           tc_fence_after();
           for (uint32_t fresh = 1; kb < end; ++kb, ++it, fresh = 0) {
             const int s = it % NS;
-            if (!(ok = mbar_wait_cluster(full + s, (it / NS) & 1, abort_flag, status))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(full + s, (it / NS) & 1, abort_flag, status)))) break;
             tc_fence_after();
             const uint32_t a0 = base + s * Cfg::kStage, b0 = a0 + Cfg::kA;
             const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
             const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              umma<CG>(tmem + acc * kBN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
-                       idesc, kk > 0 ? 1u : 1u - fresh);
-            umma_done<CG>(empty + s);
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                umma<CG>(tmem + acc * kBN, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)),
+                         idesc, kk > 0 ? 1u : 1u - fresh);
+              umma_done<CG>(empty + s);
+            }
           }
-          if (ok) umma_done<CG>(acc_full + acc);
+          if (ok && leader) umma_done<CG>(acc_full + acc);
         }
       }
       if (!ok) {   // what was issued is done before TMEM is given back
-        umma_done<CG>(drain);
+        if (leader) umma_done<CG>(drain);
         mbar_wait_drain(drain, 0);
       }
     }
@@ -613,17 +634,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
   const int blocks = (kb1 - kb0) * (kPlanes ? 3 : 1);
   int it = 0;   // the loading thread's place
   let_next_start();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+  if (warp == 0) {
+    if (lane < NS) {
+      mbar_init(full + lane, 1);
+      mbar_init(empty + lane, 1);
+    } else if (lane == kFewMostStages) {
+      mbar_init(acc_full, 1);
+      *abort_flag = 0;
     }
-    mbar_init(acc_full, 1);
-    *abort_flag = 0;
     fence_mbar_init();
-    wait_for_previous();
-    // the first round of stages is on its way before anything else is set up
-    for (; it < NS && it < blocks; ++it) load(it, it);
+    __syncwarp();
+    if (lane == 0) {
+      wait_for_previous();
+      // the first round of stages is on its way before anything else is set up
+      for (; it < NS && it < blocks; ++it) load(it, it);
+    }
   }
   if (warp == 2) tmem_take<1>(tmem_slot, kAcc);
   wait_for_previous();
@@ -645,59 +670,67 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, FN, AMN, BMN);
-      const uint32_t base = smem_u32(smem);
-      auto product = [&](int sa, int sb, uint32_t acc, bool add) {
-        const uint32_t a0 = base + sa * stage, b0 = base + sb * stage + a_bytes;
-        const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
-        const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
+    // The whole warp walks the loop, so that what one of its threads issues comes
+    // from uniform registers (a lone thread took 130 cycles per MMA of 128 columns,
+    // twice what the tensor core takes: 8 x 4096 x 4096 10.7 us, so 8.7.  For the
+    // loads it was slower: 9.6).
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16_f32(128, FN, AMN, BMN);
+    const uint32_t base = smem_u32(smem);
+    auto product = [&](int sa, int sb, uint32_t acc, bool add) {
+      const uint32_t a0 = base + sa * stage, b0 = base + sb * stage + a_bytes;
+      const SDesc da = AMN ? sdesc_sw128_split(a0, 8192, 1024) : sdesc_sw128_split(a0, 16, 1024);
+      const SDesc db = BMN ? sdesc_sw128_split(b0, 8192, 1024) : sdesc_sw128_split(b0, 16, 1024);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
           umma<1>(acc, sdesc_at(da, kk * (AMN ? 2048 : 32)), sdesc_at(db, kk * (BMN ? 2048 : 32)), idesc,
                   add || kk > 0 ? 1u : 0u);
-      };
-      uint32_t phase = 0;
-      int s = 0;
-      auto arrived = [&] {
-        if (!mbar_wait(full + s, phase, abort_flag, status)) return false;
-        tc_fence_after();
-        return true;
-      };
-      auto next = [&] {
-        if (++s == NS) s = 0, phase ^= 1;
-      };
-      if constexpr (!kPlanes) {
-        for (int it = 0; it < blocks; ++it, next()) {
-          if (!arrived()) break;
-          product(s, s, tmem, it > 0);
-          umma_done<1>(empty + s);
-        }
-      } else {
-        for (int it = 0; it < blocks; it += 3) {
-          const bool add = it > 0;
-          if (!arrived()) break;
-          const int mid = s;
-          product(mid, mid, tmem + FN, add);
-          next();
-          if (!arrived()) break;
-          const int first = s;
-          product(first, mid, tmem + FN, true);
-          product(mid, first, tmem + FN, true);
-          umma_done<1>(empty + mid);
-          product(first, first, tmem, add);
-          next();
-          if (!arrived()) break;
-          product(first, s, tmem + FN, true);
-          product(s, first, tmem + FN, true);
-          umma_done<1>(empty + first);
-          umma_done<1>(empty + s);
-          next();
-        }
       }
-      umma_done<1>(acc_full);   // also after an abort: what was issued is done before TMEM is given back
-      mbar_wait_drain(acc_full, 0);
+    };
+    uint32_t phase = 0;
+    int s = 0;
+    auto arrived = [&] {
+      if (!__all_sync(0xffffffffu, mbar_wait(full + s, phase, abort_flag, status))) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto done = [&](uint64_t* bar) {
+      if (leader) umma_done<1>(bar);
+    };
+    auto next = [&] {
+      if (++s == NS) s = 0, phase ^= 1;
+    };
+    if constexpr (!kPlanes) {
+      for (int it = 0; it < blocks; ++it, next()) {
+        if (!arrived()) break;
+        product(s, s, tmem, it > 0);
+        done(empty + s);
+      }
+    } else {
+      for (int it = 0; it < blocks; it += 3) {
+        const bool add = it > 0;
+        if (!arrived()) break;
+        const int mid = s;
+        product(mid, mid, tmem + FN, add);
+        next();
+        if (!arrived()) break;
+        const int first = s;
+        product(first, mid, tmem + FN, true);
+        product(mid, first, tmem + FN, true);
+        done(empty + mid);
+        product(first, first, tmem, add);
+        next();
+        if (!arrived()) break;
+        product(first, s, tmem + FN, true);
+        product(s, first, tmem + FN, true);
+        done(empty + first);
+        done(empty + s);
+        next();
+      }
     }
+    done(acc_full);   // also after an abort: what was issued is done before TMEM is given back
+    mbar_wait_drain(acc_full, 0);
     __syncwarp();
   } else if (warp >= kEpilogueWarp) {
     const int q = warp % 4, half = (warp - kEpilogueWarp) / 4, m = q * 32 + lane;
@@ -724,46 +757,59 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
     }
   }
   tc_fence_before();
+  // this CTA's share of the columns, FN / S, in bands of 16 through the epilogue; what it reads for a
+  // thread's first band is on its way meanwhile
+  const int own_n = FN / S, bands = own_n / kBand;
+  auto band_at = [&](int i, int& m, int& c) {
+    m = i / bands;
+    c = (i - m * bands) * kBand;
+    return n0 + rank * own_n + c;
+  };
+  typename Epi::Fetched f;
+  int m, c, n = band_at(threadIdx.x, m, c);
+  if (threadIdx.x < rows * bands) ep.fetch(f, ep.row(m0 + m), n, true);
   __syncthreads();
-  cluster_sync();
   if (warp == 2) tmem_give<1>(tmem, kAcc);
-  // this CTA's share of the columns, FN / S: four at a time from every CTA into its own rows (nobody
-  // else reads those), then bands of 16 through the epilogue
-  float* own = reinterpret_cast<float*>(smem) + rank * (FN / S);
-  const int quads = FN / 4 / S, bands = FN / kBand / S;
-  for (int i = threadIdx.x; i < rows * quads && S > 1; i += kFewThreads) {
-    const int m = i / quads;
-    float4* at = reinterpret_cast<float4*>(own + m * kFewPitch<FN>) + (i - m * quads);
-    float4 w[4];
+  float* own = reinterpret_cast<float*>(smem) + rank * own_n;
+  if (S > 1) {
+    cluster_sync();
+    // four columns at a time from every CTA into this one's rows (nobody else reads those)
+    const int quads = own_n / 4;
+    for (int i = threadIdx.x; i < rows * quads; i += kFewThreads) {
+      const int r0 = i / quads;
+      float4* at = reinterpret_cast<float4*>(own + r0 * kFewPitch<FN>) + (i - r0 * quads);
+      float4 w[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (r < S)
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(w[r].x), "=f"(w[r].y), "=f"(w[r].z), "=f"(w[r].w)
-                     : "r"(map_to(at, r))
-                     : "memory");
-    float4 v = w[0];
+      for (int r = 0; r < 4; ++r)
+        if (r < S)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(w[r].x), "=f"(w[r].y), "=f"(w[r].z), "=f"(w[r].w)
+                       : "r"(map_to(at, r))
+                       : "memory");
+      float4 v = w[0];
 #pragma unroll
-    for (int r = 1; r < 4; ++r)
-      if (r < S) v.x += w[r].x, v.y += w[r].y, v.z += w[r].z, v.w += w[r].w;
-    *at = v;
+      for (int r = 1; r < 4; ++r)
+        if (r < S) v.x += w[r].x, v.y += w[r].y, v.z += w[r].z, v.w += w[r].w;
+      *at = v;
+    }
+    cluster_arrive();   // (the others' memory is read)
+    __syncthreads();
   }
-  __syncthreads();
   for (int i = threadIdx.x; i < rows * bands; i += kFewThreads) {
-    const int m = i / bands, c = (i - m * bands) * kBand, n = n0 + rank * (FN / S) + c;
+    if (i >= kFewThreads) {
+      n = band_at(i, m, c);
+      ep.fetch(f, ep.row(m0 + m), n, true);
+    }
     if (n >= g.N || *abort_flag) continue;
-    typename Epi::Fetched f;
-    const int64_t row = ep.row(m0 + m);
-    ep.fetch(f, row, n, true);
     float v[kBand];
 #pragma unroll
     for (int j = 0; j < kBand; j += 4) {
       const float4 w = *reinterpret_cast<const float4*>(own + m * kFewPitch<FN> + c + j);
       v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
     }
-    ep.put(f, row, n, 0, v);
+    ep.put(f, ep.row(m0 + m), n, 0, v);
   }
-  cluster_sync();   // the others have read this CTA's memory
+  if (S > 1) cluster_wait();   // the others have read this CTA's memory
 }
 
 // Sum of the parts' sums, then the epilogue: a thread takes 16 columns of a row.
