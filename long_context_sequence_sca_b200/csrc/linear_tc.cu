@@ -922,11 +922,11 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   // Or the few-rows kernel's tiles, of 128 or 256 columns, whose clusters are to be
   // resident all at once (33 of 4 CTAs, 74 of 2: cudaOccupancyMaxActiveClusters; 16
   // of 8 where 15 fit took 20 us against 14).  The times in us that decide were
-  // fitted to 28 products from 8 x 4096 x 4096 to 3711 x 1000 x 1288: 256 x 4096 x
-  // 4096 takes 20.5 with large tiles, 17.3 and 15.8 with these; 1024 x 1024 x 1024
-  // 12.2, 10.2 and 11.9; 1024 x 4096 x 4096 27.7, 27.3 and 31.2.  For fp32 to 30 (with
-  // the splitting): 1024 x 1024 x 1024 takes 27.0, 22.0 and 23.7; 1024 x 1024 x 4096
-  // 64.1 and, in parts of a run, 56.8 with 256 columns.
+  // fitted to 24 products from 8 x 4096 x 4096 to 4096 x 2048 x 1024: 256 x 4096 x
+  // 4096 takes 20.1 with large tiles, 13.4 and 15.5 with these; 1024 x 1024 x 1024
+  // 12.4, 8.9 and 11.6; 1024 x 4096 x 4096 27.5 and, with 256 columns, 27.5.  For
+  // fp32 to 30 (with the splitting): 1024 x 1024 x 1024 takes 27.0, 22.0 and 23.7;
+  // 1024 x 1024 x 4096 64.1 and, in parts of a run, 56.8 with 256 columns.
   const int64_t waves = (t * g.splits + slots - 1) / slots;
   double best = (g.splits > 1 ? 14.0 + 0.5 * g.splits : 7.5) + 0.29 * g.blocks_per_split * g.pairs * waves;
   const int64_t k_blocks = g.k_blocks;
@@ -937,7 +937,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
     if (exact && tiles(k_blocks, S) > g.run) continue;
     const double part = tiles(k_blocks, S);
     const double cost = planes == 3 ? (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
-                                    : (n == 128 ? 6.3 + 0.325 * part : 9.0 + 0.36 * part);
+                                    : (n == 128 ? 7.3 + 0.17 * part : 10.2 + 0.31 * part);
     if (cost > best && !(M <= 128 && pl.cg != 0)) continue;   // (one-CTA large tiles only where it must be)
     best = cost;
     pl.cg = 0;
