@@ -8,9 +8,9 @@ namespace gecko {
 // A call's kernels overlap at their ends: each lets the next one start as soon as
 // all its own blocks run, and waits for the one before (and so for all before that)
 // before it touches global memory, with barriers and TMEM set up by then.  A call's
-// first kernel is launched without the attribute.  (The projection's
-// gradients at 777 x 520 x 1032 in fp32, five kernels: 47 us a call without, 40 with;
-// 512 x 512 x 512 in bf16 31 and 25.)
+// first kernel is launched without the attribute.  The projection's gradients at
+// 777 x 520 x 1032 in fp32, five kernels: 47 us a call without this, 40 with it; 512
+// x 512 x 512 in bf16 31 and 25.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
