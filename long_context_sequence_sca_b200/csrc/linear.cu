@@ -405,9 +405,9 @@ cudaError_t backward_impl(const LinearProblem& p, cudaStream_t st) {
     if (tc && f32) launch_du<T, true>(p, du, pitch, sums, blocks, st);
     else launch_du<T, false>(p, du, pitch, sums, blocks, st);
     after = true;
+    const dim3 cols((unsigned)((p.N + 31) / 32));
     if (p.db && blocks > 1 &&
-        (e = launch_chained(linear_db_kernel, dim3((unsigned)((p.N + 31) / 32)), 256, 0, 0, after, st, part, (int)blocks,
-                            p.N, p.db)))
+        (e = launch_chained(linear_db_kernel, cols, 256, 0, 0, after, st, part, (int)blocks, p.N, p.db)))
       return e;
   }
   const void* g = alias ? p.dy : ws + l.du;

@@ -539,7 +539,8 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
             tmem_ld16p(lanes + acc * kBN + (j + 1) * kShare * kBand, v[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 2 * kBand; ++i) sum[j + i / kBand][i % kBand] += __uint_as_float(v[i / kBand][i % kBand]);
+            for (int i = 0; i < 2 * kBand; ++i)
+              sum[j + i / kBand][i % kBand] += __uint_as_float(v[i / kBand][i % kBand]);
           }
           // the accumulator is read: the run after next may write it
           tc_fence_before();

@@ -799,8 +799,8 @@ cudaError_t scan_impl(const ScanProblem& p, cudaStream_t st) {
   if ((e = set_args(p, p.state_in, p.state_out, &a, &chained, st))) return e;
   constexpr int smem = 2 * kTileBytes + 128;
   if ((e = cudaFuncSetAttribute(scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-  return launch_chained(scan_kernel<T>, dim3((unsigned)(a.C * a.B * a.tiles)), kThreads, smem, 0, chained, st, mx, mg, my,
-                        a);
+  return launch_chained(scan_kernel<T>, dim3((unsigned)(a.C * a.B * a.tiles)), kThreads, smem, 0, chained, st, mx, mg,
+                        my, a);
 }
 
 template <typename T>
