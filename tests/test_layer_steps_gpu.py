@@ -247,3 +247,53 @@ def test_refusals(L):
     odd = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view_as(x)
     with pytest.raises(L.GeckoError):
         L.gated_scan_forward(odd, p["log_a"])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_calls_without_a_pause(L, dtype, captured):
+    """Inputs written right before a call and overwritten right after it, several
+    calls in a row on one stream: a call's kernels overlap with each other, and with
+    nothing else.  The results are those of calls with a pause, bit for bit."""
+    n = 4
+    ps = [_layer_inputs(2, 300, 2, 64, dtype, seed=20 + i) for i in range(n)]
+    now = {k: torch.empty_like(v) for k, v in ps[0].items()}
+
+    def calls(p):
+        y, st, ch = L.gated_scan_forward(p["x"], p["log_a"], return_state=True, keep_chunks=True)
+        dx, dg, ds = L.gated_scan_backward(p["x"], p["log_a"], y, ch, dstate_out=st)
+        v, pre = L.linear_forward(p["x"], p["wv"], bias=p["bv"], act="silu", heads=2, keep_pre=True)
+        du = L.linear_backward(p["x"], p["wv"], v, pre=pre, act="silu", heads=2)
+        q = L.qk_forward(p["x"], p["scale"], p["shift"], rot_dim=64)
+        return [y, st, ch, dx, dg, ds, v, pre, *du, *q, *L.qk_backward(p["x"], p["scale"], *q, rot_dim=64)]
+
+    want = []
+    for p in ps:
+        want.append(calls(p))
+        torch.cuda.synchronize()
+
+    def row():
+        got = []
+        for p in ps:
+            for k, v in now.items():
+                v.copy_(p[k])
+            got.append(calls(now))
+            for v in now.values():
+                v.fill_(float("nan"))
+        return got
+
+    if captured:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            row()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = row()
+        for _ in range(3):
+            graph.replay()
+    else:
+        got = row()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for s, t in zip(a, b):
+            assert torch.equal(s, t)
