@@ -157,3 +157,26 @@ def test_two_dimensional_input(L):
     y = L.linear_forward(inp["x"], inp["w"], bias=inp["bias"], residual=inp["residual"], act="silu")
     y2 = L.linear_forward(inp["x"][0], inp["w"], bias=inp["bias"], residual=inp["residual"][0], act="silu")
     assert y2.shape == (37, 64) and torch.equal(y2, y[0])
+
+
+@pytest.mark.parametrize("T,N,K", [(17, 136, 8), (100, 72, 4096), (700, 264, 72), (1024, 1024, 1024), (120, 1024, 2056),
+                                   (640, 1000, 4096), (2100, 1032, 520), (4096, 64, 200)])
+def test_fp32_products_are_as_good_as_fp32(L, T, N, K):
+    """In the norm.  A step of 16 products cuts about 2^-25.5 of the sum, always to
+    zero, and at most 64 steps follow one another before the sums are rounded:
+    2^-19.5 together, far above what the roundings add (their signs differ).
+    Without the third planes the products would be off by 2^-18 and more."""
+    inp = _inputs(1, T, N, K, 0, "f32", seed=T + N + K, bias=False, residual=False)
+    hx, hw, hd = (host(inp[k])[0] if k != "w" else host(inp[k]) for k in ("x", "w", "dy"))
+    y = L.linear_forward(inp["x"], inp["w"])
+    dx, dw, _ = L.linear_backward(inp["x"], inp["w"], inp["dy"])
+    for got, want in ((y, hx @ hw.T), (dx, hd @ hw), (dw, hd.T @ hx)):
+        err = np.linalg.norm(host(got).reshape(want.shape) - want) / np.linalg.norm(want)
+        assert err <= 2.0 ** -19, err
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K,H", [(100, 72, 4096, 0), (640, 1000, 4096, 0), (120, 1024, 2056, 8), (260, 4096, 520, 0)])
+def test_shared_depth(L, T, N, K, H, dtype):
+    """Clusters of two and four CTAs, parts of one run and of several, ragged rows and columns."""
+    check(L, _inputs(1, T, N, K, H, dtype, seed=T + K), dtype, "gelu", H)
