@@ -908,7 +908,9 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   // Large tiles.  Few of them: as many parts as fill the GPU, each of eight
   // k-blocks' work at least (below 32 the second kernel costs more than the
   // parts save).
-  pl.cg = M <= 128 ? 1 : 2;
+  // (Up to 128 rows fill half a pair's tile, but of much depth the parts gain more: dw of
+  // 64 x 912 over 81920 tokens 87 us with the few-rows kernel, 51 so.)
+  pl.cg = exact && M <= 128 ? 1 : 2;
   g.tiles_m = tiles(M, 128 * pl.cg);
   const int64_t slots = sm_count() / pl.cg, t = (int64_t)g.tiles_m * g.tiles_n;
   const int64_t work = (int64_t)g.k_blocks * g.pairs;   // k-blocks of a tile
@@ -939,7 +941,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
     const double part = tiles(k_blocks, S);
     const double cost = planes == 3 ? (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
                                     : (n == 128 ? 7.3 + 0.17 * part : 10.2 + 0.31 * part);
-    if (cost > best && !(M <= 128 && pl.cg != 0)) continue;   // (one-CTA large tiles only where it must be)
+    if (cost > best && pl.cg != 1) continue;   // (one-CTA large tiles only where it must be)
     best = cost;
     pl.cg = 0;
     pl.few_n = n;
@@ -1037,8 +1039,13 @@ cudaError_t forward_tc(const LinearProblem& p, const void* xp, const void* wp, v
 }  // namespace
 
 size_t gemm_tc_workspace(int64_t M, int64_t N, int64_t K, int dtype) {
-  const GemmPlan pl = gemm_plan(M, N, K, dtype == kBF16 ? 1 : 3, true);
-  return pl.cg == 0 || pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
+  size_t most = 0;
+  for (bool exact : {false, true}) {
+    const GemmPlan pl = gemm_plan(M, N, K, dtype == kBF16 ? 1 : 3, exact);
+    const size_t n = pl.cg == 0 || pl.g.splits == 1 ? 0 : sizeof(float) * (size_t)pl.g.splits * M * N;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, const void* x, const void* w, void* ws, bool after,

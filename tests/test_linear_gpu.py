@@ -180,3 +180,10 @@ def test_fp32_products_are_as_good_as_fp32(L, T, N, K):
 def test_shared_depth(L, T, N, K, H, dtype):
     """Clusters of two and four CTAs, parts of one run and of several, ragged rows and columns."""
     check(L, _inputs(1, T, N, K, H, dtype, seed=T + K), dtype, "gelu", H)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(20000, 64, 264), (30011, 128, 72)])
+def test_many_tokens_few_features(L, T, N, K, dtype):
+    """dw and dx of much depth or many rows and hardly any columns."""
+    check(L, _inputs(1, T, N, K, 0, dtype, seed=T, residual=False), dtype, "silu", 0)
