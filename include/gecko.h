@@ -369,8 +369,10 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
  * whose gates depend on the input (CEMA's alpha, delta and theta are fixed
  * parameters of the layer).  Per batch b and feature d:
  *   a_t = exp(log_a_t), h_t = a_t h_{t-1} + x_t, y_t = h_t
- * held in fp32.  A gate of log_a = -inf (or low enough that exp is 0), or a
- * document start at token t (reset), drops the first term: h_t = x_t.
+ * held in fp32.  A gate of log_a = -inf (or low enough that exp is 0 in fp32; in
+ * bf16 tensors below 2^-126), or a document start at token t (reset), drops the
+ * first term: h_t = x_t, whatever h_{t-1} and the gates before are.  Open gates keep
+ * a NaN or an infinity in the state, however small their product is.
  *
  *   x, log_a, y : [B, L, D] dtype `dtype`; y may equal x.  log_a <= 0 is what
  *                 the operator is for and is not checked; growing gates work

@@ -103,6 +103,14 @@ __device__ __forceinline__ void write4(uint8_t* p, typename Lane<T>::Raw v) {
 // A decay of zero drops what came before, even if that is not finite.
 __device__ __forceinline__ float decay_fma(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
 
+// The decay over several tokens.  It is zero only where one of the gates is: open
+// gates keep a NaN or an infinity in the state, however small their product, so that
+// is held at the smallest subnormal (what a finite state adds through it is below 2^-149
+// of that state).
+constexpr float kLeastDecay = 1.4e-45f;
+__device__ __forceinline__ float held(float a) { return a == 0.f ? kLeastDecay : a; }   // (of open gates)
+__device__ __forceinline__ float join_decays(float a, float b) { return a == 0.f || b == 0.f ? 0.f : held(a * b); }
+
 // log_a above this: the gate is not zero.
 constexpr float kOpen = -87.f;
 
@@ -266,7 +274,7 @@ __device__ __forceinline__ bool gather(const ScanArgs& a, const Tile& t, const P
         if (c0 + c < p.n) {
           const float ca = __uint_as_float((uint32_t)w[c][i]);
           h = decay_fma(ca, h, __uint_as_float((uint32_t)(w[c][i] >> 32)));
-          A *= ca;
+          A = join_decays(A, ca);
         }
     sm.pre[warp][f + i] = make_float2(A, h);
     if (warp == 0) {
@@ -341,17 +349,37 @@ __device__ __forceinline__ typename Lane<T>::Val step(typename Lane<T>::Val a, t
   return X::put(hv);
 }
 
+// v, 0 where a is zero.
+template <typename T, bool kShut>
+__device__ __forceinline__ typename Lane<T>::Val passed(typename Lane<T>::Val a, typename Lane<T>::Val v) {
+  using X = Lane<T>;
+  if (!kShut) return v;
+  float av[kV<T>], vv[kV<T>];
+  X::get(a, av);
+  X::get(v, vv);
+#pragma unroll
+  for (int i = 0; i < kV<T>; ++i) vv[i] = av[i] == 0.f ? 0.f : vv[i];
+  return X::put(vv);
+}
+
 // a b, 0 where a is zero.
 template <typename T, bool kShut>
 __device__ __forceinline__ typename Lane<T>::Val times(typename Lane<T>::Val a, typename Lane<T>::Val b) {
+  return passed<T, kShut>(a, Lane<T>::mul(a, b));
+}
+
+// The decays' product, one token on.  (kShut = false: zero once it underflows, which
+// is looked at behind the span.)
+template <typename T, bool kShut>
+__device__ __forceinline__ typename Lane<T>::Val next_decay(typename Lane<T>::Val A, typename Lane<T>::Val g) {
   using X = Lane<T>;
-  if (!kShut) return X::mul(a, b);
-  float av[kV<T>], bv[kV<T>];
-  X::get(a, av);
-  X::get(b, bv);
+  if (!kShut) return X::mul(A, g);
+  float Av[kV<T>], gv[kV<T>];
+  X::get(A, Av);
+  X::get(g, gv);
 #pragma unroll
-  for (int i = 0; i < kV<T>; ++i) bv[i] = av[i] == 0.f ? 0.f : av[i] * bv[i];
-  return X::put(bv);
+  for (int i = 0; i < kV<T>; ++i) Av[i] = join_decays(Av[i], gv[i]);
+  return X::put(Av);
 }
 
 // The map of a span: A the product of its gates, h its scan from zero; for the
@@ -372,21 +400,38 @@ __device__ __forceinline__ float span_map(const uint8_t* pg, const uint8_t* px, 
     low = X::least(low, raw);
     const typename X::Val g = gate_at<T, kShut>(raw, starts, s);
     h = step<T, kShut>(g, h, X::open(read4<T>(px + s * kRowBytes)));
-    A = X::mul(A, g);
+    A = next_decay<T, kShut>(A, g);
     if (kBack) e = X::add(e, times<T, kShut>(A, X::open(read4<T>(pd + s * kRowBytes))));
   }
   return X::lowest(low);
 }
 
 // Whether the careful form is needed, decided for the warp; the map that goes
-// with it.
+// with it.  (The map alone also needs it where an infinite output gradient met a
+// product of open gates that had underflowed, as a NaN shows.)
 template <typename T, bool kBack>
 __device__ __forceinline__ bool span_map_of(const uint8_t* pg, const uint8_t* px, const uint8_t* pd, uint32_t starts,
                                             typename Lane<T>::Val& A, typename Lane<T>::Val& h,
                                             typename Lane<T>::Val& e) {
-  if (!starts && __all_sync(0xffffffffu, span_map<T, false, kBack>(pg, px, pd, 0, A, h, e) > kOpen)) return false;
-  span_map<T, true, kBack>(pg, px, pd, starts, A, h, e);
-  return true;
+  using X = Lane<T>;
+  const bool open =
+      !starts && __all_sync(0xffffffffu, span_map<T, false, kBack>(pg, px, pd, 0, A, h, e) > kOpen);
+  bool whole = open;
+  if (open) {
+    float v[kV<T>], ev[kV<T>];
+    X::get(A, v);
+    X::get(e, ev);
+    bool lost = false;
+#pragma unroll
+    for (int i = 0; i < kV<T>; ++i) {
+      lost |= v[i] == 0.f && isnan(ev[i]);
+      v[i] = held(v[i]);
+    }
+    A = X::put(v);
+    if (kBack) whole = !__any_sync(0xffffffffu, lost);
+  }
+  if (!whole) span_map<T, true, kBack>(pg, px, pd, starts, A, h, e);
+  return !open;
 }
 
 // y over the consumed x.
@@ -464,7 +509,7 @@ __device__ __forceinline__ void fold(const float2 (&map)[kWarps][F], int f, int 
     for (int i = 0; i < V; ++i) {
       const float2 m = map[w][f + i];
       h[i] = decay_fma(m.x, h[i], m.y);
-      A[i] *= m.x;
+      A[i] = join_decays(A[i], m.x);
     }
 }
 

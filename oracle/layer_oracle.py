@@ -52,7 +52,7 @@ def gated_scan_grad(x, log_a, dy, state=None, reset=None, dstate=None):
     for t in range(L - 1, -1, -1):
         dx[:, t] = dy[:, t] + back
         back = _times(a[:, t], dx[:, t])
-        dg[:, t] = dx[:, t] * _times(a[:, t], before[:, t])
+        dg[:, t] = _times(a[:, t], dx[:, t] * before[:, t])
     return dx, dg, back
 
 
