@@ -489,8 +489,8 @@ __device__ __forceinline__ void span_back(uint8_t* pg, uint8_t* pd, uint32_t sta
       const typename X::Val dh = X::add(X::open(dy[i]), e);
       e = times<T, kShut>(a, dh);
       dy[i] = X::shut(dh);
-      // (where the gate is zero e is, and before may not be finite)
-      g[i] = X::shut(times<T, kShut>(e, before[s0 + i]));
+      // (where the gate is zero before may not be finite)
+      g[i] = X::shut(passed<T, kShut>(a, X::mul(e, before[s0 + i])));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

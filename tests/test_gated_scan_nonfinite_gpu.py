@@ -125,6 +125,18 @@ def test_shut_gate_ends_it(L, at, log_a, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_gradient_does_not_hide_it(L, dtype):
+    """dlog_a = dh a h is NaN where h is and the gate is open, also for dh = 0 and beside a shut gate."""
+    inp = _decaying(200, 16, dtype, -0.5, seed=34)
+    inp["reset"] = torch.zeros(2, 200, dtype=torch.uint8, device="cuda")
+    inp["reset"][0, 75] = 1
+    inp["x"][:, 64, :8] = torch.nan
+    inp["dy"].zero_()
+    inp["dstate"].zero_()
+    check(L, inp, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_segments_keep_it_too(L, dtype):
     """A sequence in segments, down to one token, has the same NaN and infinities as the whole."""
     inp = _decaying(1000, 16, dtype, -1.0, seed=35)
