@@ -449,12 +449,14 @@ int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, con
  *   u = x w^T + bias,  y = f(u) + residual
  * with f the identity, SiLU u / (1 + e^-u) or GELU u Phi(u) (Phi the normal
  * distribution function).  fp32 accumulation; one rounding of y.  (The tensor
- * core cuts its fp32 sums: 2^-25.5 of the sum a step of 16 on average, invisible
- * in bf16 results; fp32 ones are summed in runs of at most 2048.)  fp32 operands
- * are split into three bf16 parts and multiplied on the tensor cores as six
- * partial products: as accurate as fp32 FMA (a few 2^-24 per term; measured
- * 1e-7 to 2e-6 of the result's norm), except that an infinite operand gives
- * NaN where IEEE arithmetic might give an infinity.
+ * core cuts its fp32 sums, which draws them towards zero: by 2^-25.5 of the result
+ * every 16 terms, 2^-23.5 where all terms have one sign.  bf16 results are summed
+ * in runs of at most 8192 of the depth and lose 4e-5 of themselves at most, 1/100 of
+ * their rounding; fp32 ones, pre among them, in runs of at most 2048, and lose 5e-6
+ * at most.)  fp32 operands are split into three bf16 parts and multiplied on the
+ * tensor cores as six partial products: as accurate as fp32 FMA (a few 2^-24 per
+ * term; measured 1e-7 to 2e-6 of the result's norm), except that an infinite
+ * operand gives NaN where IEEE arithmetic might give an infinity.
  *
  *   x        : [B, T, K] dtype `dtype`.
  *   w        : [N, K] dtype.

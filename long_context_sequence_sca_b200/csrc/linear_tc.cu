@@ -9,12 +9,13 @@
 // product six times as deep whose k-blocks come from different planes; at a sixth
 // of the bf16 rate this is still several times the rate of the fp32 FMA pipe.
 //
-// The tensor core cuts its sums instead of rounding them, by about 2^-25.5 of
-// the sum a step (measured: 5e-6 of the result after 256 steps, which shows in
-// the fp32 results: y, pre, db).  Where it would (fp32, and bf16 with pre), a
-// product is cut into runs of 1024 (2048), whose sums the epilogue warps add up
-// in registers with rounding while the next run is under way (kSum), and the
-// planes are added in ascending size, or apart from the first.
+// The tensor core cuts its sums instead of rounding them: a step of 16 terms takes
+// about 2^-25.5 of the result, 2^-23.5 where all terms have one sign (measured:
+// 6e-6 and 1.6e-5 after 256 steps, which shows in the fp32 results: y, pre, db).  Where it would (fp32, bf16 with pre, and any bf16
+// product that is deeper than kDeep), a product is cut into runs of 1024 (2048; kDeep),
+// whose sums the epilogue warps add up in registers with rounding while the next run is
+// under way (kSum), and the planes are added in ascending size, or apart from the
+// first.
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
 // ring of stages, one thread issues tcgen05.mma, eight or sixteen warps empty the
@@ -892,9 +893,17 @@ struct GemmPlan {
   GemmShape g;
 };
 
+// k-blocks that the sums of a bf16 result may be cut over: 8192 of the depth, which
+// draw a sum of positive terms towards zero by 3.6e-5 (measured; 1/100 of a rounding
+// to bf16), one of random signs by 1e-5.  Never emptied, the accumulator took 7.9e-4 off a
+// sum of 131072 positive terms, and 6e-3 off one of a million.  Emptying it costs nothing where
+// every pair has a tile (dw of 4096 x 4096 over 65536 tokens 1554 us without, 1557 with;
+// with runs of 2048 1577), and 5 to 10 % with 40 tiles for 74 pairs (2048 x 1032).
+constexpr int kDeep = 128;
+
 // exact: the sums of the accumulator's runs are to be rounded, not cut.  A part
 // of one run needs no adding up (of fp32, one run of the last plane product: the
-// ones before it are small).
+// ones before it are small); nor does one of kDeep for a result rounded to bf16.
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   GemmPlan pl;
   auto tiles = [](int64_t x, int64_t t) { return (int)((x + t - 1) / t); };
@@ -904,7 +913,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   g.tiles_n = tiles(N, kBN);
   g.k_blocks = tiles(K, kBK);
   g.pairs = planes == 3 ? kPairs : 1;
-  g.run = planes == 3 ? 16 : 32;
+  g.run = planes == 3 ? 16 : exact ? 32 : kDeep;
   // Large tiles.  Few of them: as many parts as fill the GPU, each of eight
   // k-blocks' work at least (below 32 the second kernel costs more than the
   // parts save).
@@ -920,7 +929,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   if (splits < 1) splits = 1;
   g.blocks_per_split = (int)((g.k_blocks + splits - 1) / splits);
   g.splits = (g.k_blocks + g.blocks_per_split - 1) / g.blocks_per_split;
-  pl.sum = exact && g.blocks_per_split > g.run;
+  pl.sum = g.blocks_per_split > g.run;
 
   // Or the few-rows kernel's tiles, of 128 or 256 columns, whose clusters are to be
   // resident all at once (33 of 4 CTAs, 74 of 2: cudaOccupancyMaxActiveClusters; 16
@@ -937,7 +946,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
     const int64_t few_tiles = (int64_t)tiles(M, 128) * tiles(N, n);
     if (few_tiles > sm_count() && (M > 128 || n == 256)) continue;
     const int S = few_tiles <= 33 && k_blocks >= 8 ? 4 : few_tiles <= 74 && k_blocks >= 4 ? 2 : 1;
-    if (exact && tiles(k_blocks, S) > g.run) continue;
+    if (tiles(k_blocks, S) > g.run) continue;
     const double part = tiles(k_blocks, S);
     const double cost = planes == 3 ? (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
                                     : (n == 128 ? 7.3 + 0.17 * part : 10.2 + 0.31 * part);
@@ -1003,14 +1012,14 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
   auto product = [&](const auto& out) -> cudaError_t {
     using Out = std::decay_t<decltype(out)>;
     if constexpr (kExact) {
-      if (pl.sum)
-        return pl.cg == 2 ? run_gemm<2, AMN, BMN, true, Out>(pl, ma, mb, out, status, after, st)
-                          : run_gemm<1, AMN, BMN, true, Out>(pl, ma, mb, out, status, after, st);
       // (one CTA per tile: only where the few-rows kernel would not be exact)
-      if (pl.cg == 1) return run_gemm<1, AMN, BMN, false, Out>(pl, ma, mb, out, status, after, st);
+      if (pl.cg == 1)
+        return pl.sum ? run_gemm<1, AMN, BMN, true, Out>(pl, ma, mb, out, status, after, st)
+                      : run_gemm<1, AMN, BMN, false, Out>(pl, ma, mb, out, status, after, st);
     }
     if (pl.cg != 2) return cudaErrorInvalidValue;   // (the maps are made for pl.cg)
-    return run_gemm<2, AMN, BMN, false, Out>(pl, ma, mb, out, status, after, st);
+    return pl.sum ? run_gemm<2, AMN, BMN, true, Out>(pl, ma, mb, out, status, after, st)
+                  : run_gemm<2, AMN, BMN, false, Out>(pl, ma, mb, out, status, after, st);
   };
   if (pl.g.splits == 1) return product(ep);
   float* part = static_cast<float*>(ws);
