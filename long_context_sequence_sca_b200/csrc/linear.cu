@@ -73,7 +73,7 @@ struct ForwardOut {
     if (bias) u += bias[n];
     const int64_t at = lay.at(m, n);
     if (pre) pre[at] = u;
-    float v = activate(u, act);
+    float v = activate<T>(u, act);
     if (residual) v += to_f32(residual[at]);
     y[at] = from_f32<T>(v);
   }

@@ -299,10 +299,10 @@ struct EpiForward {
     }
     if (act == kActSilu) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = activate(v[i], kActSilu);
+      for (int i = 0; i < 16; ++i) v[i] = activate<T>(v[i], kActSilu);
     } else if (act == kActGelu) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = activate(v[i], kActGelu);
+      for (int i = 0; i < 16; ++i) v[i] = activate<T>(v[i], kActGelu);
     }
     if (residual) {
 #pragma unroll
