@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256, kDuBlocks) linear_du_kernel(const T* dy, 
       if (kAct != kActNone) {
         u.get(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], act_slope(w[j], kAct));   // (not fused into the sum below)
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], act_slope<T>(w[j], kAct));   // (not fused into the sum below)
       }
       if (du) {
         if (kPlanes) store_planes(static_cast<__nv_bfloat16*>(du) + m * pitch + n, M * pitch, v);

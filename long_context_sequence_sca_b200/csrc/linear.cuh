@@ -41,12 +41,23 @@ __device__ __forceinline__ float normal_cdf(float u, float& e) {
   return u < 0.f ? tail : 1.f - tail;
 }
 
-// f(u), of which values of type T are made: SiLU u / (1 + e^-u); GELU u Phi(u).  The
-// approximate exponential and quotient are good to 2^-21 + |u| 2^-23, far below a
-// bf16 step and enough for fp32.
+// s = 1 / (1 + e^-u) and 1 - s in fp32, both to 2^-22 of themselves.
+__device__ __forceinline__ float sigmoid(float u, float& rest) {
+  const float e = expf(-fabsf(u)), r = 1.f / (1.f + e), far = e * r;
+  rest = u < 0.f ? r : far;
+  return u < 0.f ? far : r;
+}
+
+// f(u), of which values of type T are made: SiLU u / (1 + e^-u); GELU u Phi(u).  For
+// bf16 SiLU's exponential and quotient are the SFU's, good to 2^-21 + |u| 2^-23, far
+// below a bf16 step.
 template <typename T>
 __device__ __forceinline__ float activate(float u, int act) {
-  if (act == kActSilu) return __fdividef(u, 1.f + __expf(-u));
+  if (act == kActSilu) {
+    if (sizeof(T) == 2) return __fdividef(u, 1.f + __expf(-u));
+    float rest;
+    return u * sigmoid(u, rest);
+  }
   if (act == kActGelu) {
     float e;
     return u * normal_cdf<sizeof(T) == 4>(u, e);
@@ -55,10 +66,16 @@ __device__ __forceinline__ float activate(float u, int act) {
 }
 
 // f'(u): SiLU s (1 + u (1 - s)), s = 1 / (1 + e^-u); GELU Phi(u) + u phi(u).
+template <typename T>
 __device__ __forceinline__ float act_slope(float u, int act) {
   if (act == kActSilu) {
-    const float s = __fdividef(1.f, 1.f + __expf(-u));
-    return s * fmaf(u, 1.f - s, 1.f);
+    if (sizeof(T) == 2) {
+      const float s = __fdividef(1.f, 1.f + __expf(-u));
+      return s * fmaf(u, 1.f - s, 1.f);
+    }
+    float rest;
+    const float s = sigmoid(u, rest);
+    return s * fmaf(u, rest, 1.f);
   }
   if (act == kActGelu) {
     float e;
