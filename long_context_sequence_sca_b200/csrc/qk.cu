@@ -197,13 +197,18 @@ __device__ __forceinline__ void turn8(P4& p, const Turn& r, int src) {
   }
 }
 
-// The SFU's root and reciprocal: within a unit or two of the last place.
+// Root and reciprocal, once a row: rounded ones for fp32 tensors, for bf16 the SFU's,
+// within a unit or two of the last place.
+template <typename T>
 __device__ __forceinline__ float root(float x) {
+  if (sizeof(T) == 4) return sqrtf(x);
   float y;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+template <typename T>
 __device__ __forceinline__ float reciprocal(float x) {
+  if (sizeof(T) == 4) return 1.f / x;
   float y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
@@ -304,8 +309,8 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks) qk_kernel(const __gri
     P4 z = z0.get();
     z0 = z1;
     if (s.on && k + 2 * a.token_slots < len) z1.load(zp + (k + 2 * a.token_slots) * zrow);
-    const float nrm = root(row_sum<D>(dot8(z, z)));
-    const float inv = reciprocal(nrm < a.eps ? a.eps : nrm);   // (a NaN stays)
+    const float nrm = root<T>(row_sum<D>(dot8(z, z)));
+    const float inv = reciprocal<T>(nrm < a.eps ? a.eps : nrm);   // (a NaN stays)
 #pragma unroll
     for (int i = 0; i < 4; ++i) z.v[i] = fmul2(z.v[i], pack2(inv, inv));
     Turn turn;
@@ -417,8 +422,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) qk_bwd_kernel(const _
     }
     if (++stage == S) stage = 0;
     g.zero();
-    const float nrm = root(row_sum<D>(dot8(z, z)));
-    const float inv = reciprocal(nrm < a.eps ? a.eps : nrm);   // (a NaN stays)
+    const float nrm = root<T>(row_sum<D>(dot8(z, z)));
+    const float inv = reciprocal<T>(nrm < a.eps ? a.eps : nrm);   // (a NaN stays)
     const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) z.v[i] = fmul2(z.v[i], inv2);

@@ -175,3 +175,15 @@ def test_autograd_matches_differences(L):
         # 1536 outputs of about 1, each rounded to 2^-24: noise 2^-24 sqrt(6144) / 2^-7 < 1e-3; the second-order
         # term of the unit norm (|z| about 8, |v| about 8) is about h^2 of the slope's terms, below 1e-2
         assert abs(diff - slope) <= 2e-2 * max(1.0, abs(slope)), (i, diff, slope)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_norm_is_rounded(L, d):
+    """A row of one value v of 12 bits: v^2 and its root are exact, so z' = v fl(1 / v), of which the reciprocal's
+    rounding leaves 1 or the number below it (above 1 the next is 2^-23 away, and 1 + 2^-24 rounds to 1)."""
+    v = torch.arange(2048, 4096, device="cuda").float() * 2.0 ** -9
+    z = torch.zeros(1, 2048, d, device="cuda")
+    z[0, :, 5] = torch.where(torch.arange(2048, device="cuda") % 2 == 0, v, -v)
+    scale, shift = torch.ones(4, 1, d, device="cuda"), torch.zeros(4, 1, d, device="cuda")
+    for out in L.qk_forward(z, scale, shift):
+        assert ((out[0, 0, :, 5].double().abs() - 1).abs() <= F32).all()
