@@ -11,11 +11,11 @@
 //
 // The tensor core cuts its sums instead of rounding them: a step of 16 terms takes
 // about 2^-25.5 of the result, 2^-23.5 where all terms have one sign (measured:
-// 6e-6 and 1.6e-5 after 256 steps, which shows in the fp32 results: y, pre, db).  Where it would (fp32, bf16 with pre, and any bf16
-// product that is deeper than kDeep), a product is cut into runs of 1024 (2048; kDeep),
-// whose sums the epilogue warps add up in registers with rounding while the next run is
-// under way (kSum), and the planes are added in ascending size, or apart from the
-// first.
+// 6e-6 and 1.6e-5 after 256 steps, which shows in the fp32 results: y, pre, db).
+// Where it would (fp32, bf16 with pre, and any bf16 product that is deeper than
+// kDeep), a product is cut into runs of 1024 (2048; kDeep), whose sums the epilogue
+// warps add up in registers with rounding while the next run is under way (kSum),
+// and the planes are added in ascending size, or apart from the first.
 //
 // Persistent, warp-specialised: one thread loads 64-deep k-blocks by TMA into a
 // ring of stages, one thread issues tcgen05.mma, eight or sixteen warps empty the

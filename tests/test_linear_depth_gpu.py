@@ -36,9 +36,10 @@ def _unbiased(got, want, cut):
 CUT = 2.0 ** -14
 
 
-@pytest.mark.parametrize("M,N,K", [(1 << 21, 512, 264), (1_000_003, 2048, 1032), (400_000, 128, 136), (300_001, 1200, 96)])
+@pytest.mark.parametrize("M,N,K", [(1 << 21, 512, 264), (1_000_003, 2048, 1032), (400_000, 128, 136),
+                                   (300_001, 1200, 96)])
 def test_weight_gradient(L, M, N, K):
-    """dw over 300 thousand to two million tokens: with its depth in parts, and with whole tiles for every pair of SMs."""
+    """dw over 300 thousand to two million tokens: with its depth in parts, and with whole tiles."""
     x, dy = _positive(M, K, 1), _positive(M, N, 2)
     w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
     _, dw, _ = L.linear_backward(x, w, dy, need=(False, True, False))
