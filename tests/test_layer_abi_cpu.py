@@ -119,3 +119,12 @@ def test_workspace_queries(so):
     assert L.gecko_qk_workspace(0, 100, 3, 64, 1, out) == 1
     assert L.gecko_gated_scan_workspace(2, 5000, 63, 1, 1, out) == 2
     assert L.gecko_qk_workspace(2, 100, 3, 64, 1, None) == 1
+
+
+def test_scan_length_limit(so):
+    """65535 chunks of 128 tokens, and not one token more."""
+    n = ctypes.c_int64(-1)
+    most = 65535 * L.SCAN_CHUNK
+    assert L.gecko_gated_scan_workspace(1, most, 64, 1, 1, ctypes.byref(n)) == 0 and n.value > 0
+    assert L.gecko_gated_scan_workspace(1, most + 1, 64, 1, 1, ctypes.byref(n)) == 2
+    assert _scan(Lt=most + 1) == 2 and _scan_bwd(Lt=most + 1) == 2 and L.gecko_last_error()
