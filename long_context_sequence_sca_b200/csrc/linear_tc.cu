@@ -939,17 +939,23 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
   // 12.4, 8.9 and 11.6; 1024 x 4096 x 4096 27.5 and, with 256 columns, 27.5.  For
   // fp32 to 30 (with the splitting): 1024 x 1024 x 1024 takes 27.0, 22.0 and 23.7;
   // 1024 x 1024 x 4096 64.1 and, in parts of a run, 56.8 with 256 columns.
+  // Up to 128 rows, 128 columns may also come in waves, all but the first bound by the
+  // weights' bytes, as large tiles' are there: 8 x 20480 x 4096 takes 39.5 us in two waves and
+  // 33.1 with 256 columns in one, 8 x 65536 x 4096 90 in four and 112 with large tiles.
   const int64_t waves = (t * g.splits + slots - 1) / slots;
-  double best = (g.splits > 1 ? 14.0 + 0.5 * g.splits : 7.5) + 0.29 * g.blocks_per_split * g.pairs * waves;
+  const double block = M <= 128 && waves > 1 ? 0.45 : 0.29;
+  double best = (g.splits > 1 ? 14.0 + 0.5 * g.splits : 7.5) + block * g.blocks_per_split * g.pairs * waves;
   const int64_t k_blocks = g.k_blocks;
   for (int n : {128, 256}) {
     const int64_t few_tiles = (int64_t)tiles(M, 128) * tiles(N, n);
     if (few_tiles > sm_count() && (M > 128 || n == 256)) continue;
     const int S = few_tiles <= 33 && k_blocks >= 8 ? 4 : few_tiles <= 74 && k_blocks >= 4 ? 2 : 1;
     if (tiles(k_blocks, S) > g.run) continue;
-    const double part = tiles(k_blocks, S);
-    const double cost = planes == 3 ? (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
-                                    : (n == 128 ? 7.3 + 0.17 * part : 10.2 + 0.31 * part);
+    const double part = tiles(k_blocks, S), turns = (double)((few_tiles + sm_count() - 1) / sm_count());
+    const double cost = planes == 3  ? turns * (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
+                        : turns > 1  ? turns * (2.6 + 0.34 * part)
+                        : n == 128   ? 7.3 + 0.17 * part
+                                     : 10.2 + 0.31 * part;
     if (cost > best && pl.cg != 1) continue;   // (one-CTA large tiles only where it must be)
     best = cost;
     pl.cg = 0;
