@@ -577,12 +577,15 @@ __global__ void __launch_bounds__(kGemmThreads<kSum>, 1) gemm_tc_kernel(const __
 // holds only the rows there are (to a multiple of 8): the MMA reads 128 all the
 // same, the others from the operand behind, and their results are not used.  (8 x
 // 4096 x 4096: 13.4 us with six whole stages, with eleven short ones 12.4.)
-// With kPlanes, a stage holds one plane of A and of B, loaded once for all of its
-// plane products (with a stage for each product, twice the bytes, 256 x 4096 x 1024
-// took 28.1 us against 25.7 and 64 x 4096 x 4096 70 against 58).  The order, middle
-// planes first, gives the stages back as they were taken.  The product of the
-// first planes has an accumulator to itself: as many of its sums are cut as of a
-// bf16 product's.
+// kSums says how the products are summed.  kOne: in one accumulator.  kRuns: a run of
+// g.run k-blocks has one to itself, and what is in them (up to four of 128 columns,
+// two of 256) is added up as it is read.  (Not always: with a loop over the runs 8 x
+// 4096 x 4096 took 8.4 us against 8.1.)  kPlanes3: a stage holds one plane of A and of B,
+// loaded once for all of its plane products (with a stage for each product, twice the
+// bytes, 256 x 4096 x 1024 took 28.1 us against 25.7 and 64 x 4096 x 4096 70 against
+// 58).  The order, middle planes first, gives the stages back as they were taken.  The
+// product of the first planes has an accumulator to itself: as many of its sums are
+// cut as of a bf16 product's.
 constexpr int kFewRing = 196608, kFewMostStages = 12;   // bytes of the ring
 template <int FN> constexpr int kFewPitch = FN + 4;     // floats per row left in shared memory
 constexpr int kFewMiscOff = kFewRing + (2 * kFewMostStages + 1) * 8;
@@ -595,11 +598,15 @@ __host__ __device__ constexpr int few_rows(int64_t M, bool mn) {
   return mn || M > 120 ? 128 : (int)((M + 7) / 8 * 8);
 }
 
-template <bool kPlanes, int FN, bool AMN, bool BMN, class Epi>
+enum FewSums { kOne, kRuns, kPlanes3 };
+
+template <FewSums kSums, int FN, bool AMN, bool BMN, class Epi>
 __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_constant__ CUtensorMap ma,
                                                                   const __grid_constant__ CUtensorMap mb,
                                                                   const GemmShape g, const Epi ep, int* status) {
-  constexpr int kAcc = kPlanes ? 2 * FN : FN;   // TMEM columns: the first planes' product, behind it the others
+  constexpr bool kPlanes = kSums == kPlanes3;
+  // TMEM columns: one accumulator; as many as there are; the first planes' product, behind it the others
+  constexpr int kAcc = kSums == kOne ? FN : kSums == kRuns ? 512 : 2 * FN;
   const int a_bytes = few_rows(g.M, AMN) * kBK * 2, stage = a_bytes + FN * kBK * 2;
   const int NS = min(kFewMostStages, kFewRing / stage);
   extern __shared__ uint8_t smem_raw[];
@@ -703,11 +710,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
     auto next = [&] {
       if (++s == NS) s = 0, phase ^= 1;
     };
-    if constexpr (!kPlanes) {
+    if constexpr (kSums == kOne) {
       for (int it = 0; it < blocks; ++it, next()) {
         if (!arrived()) break;
         product(s, s, tmem, it > 0);
         done(empty + s);
+      }
+    } else if constexpr (kSums == kRuns) {
+      uint32_t acc = tmem;
+      for (int it = 0, run = 0; it < blocks; ++it, next()) {
+        if (!arrived()) break;
+        product(s, s, acc, run > 0);
+        done(empty + s);
+        if (++run == g.run) run = 0, acc += FN;
       }
     } else {
       for (int it = 0; it < blocks; it += 3) {
@@ -742,14 +757,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_few_kernel(const __grid_c
       for (int c = 0; c < FN / 2; c += 32) {
         uint32_t v[32];
         tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + half * (FN / 2) + c, v);
-        if constexpr (kPlanes) {
+        if constexpr (kSums == kOne) tmem_wait_ld();
+        const int sums = kPlanes ? 2 : kSums == kOne ? 1 : (blocks + g.run - 1) / g.run;
+        for (int r = 1; r < sums; ++r) {
           uint32_t w[32];
-          tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + FN + half * (FN / 2) + c, w);
+          tmem_ld32p(tmem + ((uint32_t)(q * 32) << 16) + r * FN + half * (FN / 2) + c, w);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
-        } else {
-          tmem_wait_ld();
         }
         if (m < rows)
 #pragma unroll
@@ -889,7 +904,7 @@ cudaError_t make_map(CUtensorMap* m, const Operand& o, int planes, int64_t rows,
 struct GemmPlan {
   int cg;        // CTAs per tile; 0: the few-rows kernel
   int few_n;     // and its tiles' columns
-  bool sum;      // the accumulator's runs are added up in registers (kSum)
+  bool sum;      // the accumulator's runs are added up in registers (kSum; kRuns)
   GemmShape g;
 };
 
@@ -950,7 +965,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
     const int64_t few_tiles = (int64_t)tiles(M, 128) * tiles(N, n);
     if (few_tiles > sm_count() && (M > 128 || n == 256)) continue;
     const int S = few_tiles <= 33 && k_blocks >= 8 ? 4 : few_tiles <= 74 && k_blocks >= 4 ? 2 : 1;
-    if (tiles(k_blocks, S) > g.run) continue;
+    if (tiles(k_blocks, S) > (exact ? 1 : 512 / n) * g.run) continue;   // (512 columns of accumulators)
     const double part = tiles(k_blocks, S), turns = (double)((few_tiles + sm_count() - 1) / sm_count());
     const double cost = planes == 3  ? turns * (n == 128 ? 7.0 + 1.15 * part : 10.0 + 1.9 * part)
                         : turns > 1  ? turns * (2.6 + 0.34 * part)
@@ -960,7 +975,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int planes, bool exact) {
     best = cost;
     pl.cg = 0;
     pl.few_n = n;
-    pl.sum = false;
+    pl.sum = tiles(k_blocks, S) > g.run;
     g.tiles_m = tiles(M, 128);
     g.tiles_n = tiles(N, n);
     g.splits = S;
@@ -1010,11 +1025,15 @@ cudaError_t gemm(int64_t M, int64_t N, int64_t K, const Operand& A, const Operan
   if ((e = AMN ? make_map(&ma, A, planes, K, M, kBK)
                : make_map(&ma, A, planes, M, K, pl.cg == 0 ? few_rows(M, false) : 128))) return e;
   if ((e = BMN ? make_map(&mb, B, planes, K, N, kBK) : make_map(&mb, B, planes, N, K, b_rows))) return e;
-  if (pl.cg == 0)
-    return launch_gemm(pl.few_n == 128 ? gemm_few_kernel<planes == 3, 128, AMN, BMN, Epi>
-                                       : gemm_few_kernel<planes == 3, 256, AMN, BMN, Epi>,
-                       pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, kFewThreads, pl.g.splits, kFewAlloc, ma, mb, pl.g,
-                       ep, status, after, st);
+  if (pl.cg == 0) {
+    constexpr FewSums kSums = planes == 3 ? kPlanes3 : kOne, kDeepSums = kExact ? kSums : kRuns;
+    const auto kern = pl.few_n == 128 ? pl.sum ? gemm_few_kernel<kDeepSums, 128, AMN, BMN, Epi>
+                                               : gemm_few_kernel<kSums, 128, AMN, BMN, Epi>
+                      : pl.sum        ? gemm_few_kernel<kDeepSums, 256, AMN, BMN, Epi>
+                                      : gemm_few_kernel<kSums, 256, AMN, BMN, Epi>;
+    return launch_gemm(kern, pl.g.tiles_m * pl.g.tiles_n * pl.g.splits, kFewThreads, pl.g.splits, kFewAlloc, ma, mb,
+                       pl.g, ep, status, after, st);
+  }
   auto product = [&](const auto& out) -> cudaError_t {
     using Out = std::decay_t<decltype(out)>;
     if constexpr (kExact) {
