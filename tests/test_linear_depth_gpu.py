@@ -50,10 +50,12 @@ def test_weight_gradient(L, M, N, K):
     _unbiased(dw[cols], want, CUT)
 
 
-@pytest.mark.parametrize("M,keep_pre", [(1, False), (100, False), (100, True), (600, False)])
-def test_forward_and_input_gradient(L, M, keep_pre):
-    """y of 2^20 features, dx of 2^20."""
-    D, n = 1 << 20, 264
+@pytest.mark.parametrize("M,keep_pre,D", [(1, False, 1 << 20), (100, False, 1 << 20), (100, True, 1 << 20),
+                                          (600, False, 1 << 20), (1, False, 131072), (128, False, 100_000),
+                                          (600, False, 131072), (300, False, 33_000)])
+def test_forward_and_input_gradient(L, M, keep_pre, D):
+    """y of as many features, dx of as many."""
+    n = 264
     x, w = _positive(D, M, 3).T.contiguous(), _positive(D, n, 4).T.contiguous()
     out = L.linear_forward(x, w, keep_pre=keep_pre)
     y = out[0] if keep_pre else out

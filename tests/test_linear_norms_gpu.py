@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
 # M, N, K of y = x w^T; each is the depth of one of the three products
 SIZES = [(30011, 128, 72), (20000, 64, 264), (9, 24, 10000), (100, 136, 5000), (640, 1000, 4096), (300, 1032, 2560),
          (1100, 264, 520), (2500, 2048, 2056), (1024, 1024, 1024), (3, 4096, 1032), (129, 4104, 200), (77, 16400, 264),
-         (128, 72, 8200), (5000, 24, 16), (1, 512, 4104)]
+         (128, 72, 8200), (5000, 24, 16), (1, 512, 4104), (50000, 128, 136), (100, 264, 100000), (128, 4096, 33000),
+         (16, 40, 131072), (250, 33000, 512), (300, 264, 24008)]
 
 
 @pytest.fixture(scope="module")
