@@ -361,7 +361,8 @@ int gecko_tdnorm_forward(const void* x, void* y, const float* gamma, const float
  * are found on the host before anything is launched or written; a wait inside a
  * kernel that runs out is reported by gecko_device_status().  Returns
  * GECKO_OK, GECKO_ERR_ARG (also a workspace that is too small),
- * GECKO_ERR_SHAPE, GECKO_ERR_ALIGN or GECKO_ERR_CUDA.
+ * GECKO_ERR_SHAPE, GECKO_ERR_ALIGN, GECKO_ERR_CUDA or, where the host has no memory
+ * left, GECKO_ERR_ALLOC.
  */
 
 /*
@@ -420,7 +421,8 @@ int gecko_gated_scan_backward(const void* x, const void* log_a, const void* dy, 
  * features the pairs (a, b) become (a cos w - b sin w, b cos w + a sin w), with
  * w = pos * rot_base^(-2 i / rot_dim) for pair i, the pairs being features
  * (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved is not 0.  Angles are
- * formed in fp64.  The sum of squares is taken in fp32: it must stay finite.
+ * formed in fp64 (and good to 2^-22 up to |pos| = 2^31).  The sum of squares is taken
+ * in fp32: it must stay finite.
  *
  *   z            : [B, T, H * d] dtype `dtype`.
  *   scale, shift : [4, H, d] fp32 (q, k, q_m, k_m).
@@ -456,7 +458,11 @@ int gecko_qk_backward(const void* z, const float* scale, const int64_t* pos, con
  * at most.)  fp32 operands are split into three bf16 parts and multiplied on the
  * tensor cores as six partial products: as accurate as fp32 FMA (a few 2^-24 per
  * term; measured 1e-7 to 2e-6 of the result's norm), except that an infinite
- * operand gives NaN where IEEE arithmetic might give an infinity.
+ * operand gives NaN where IEEE arithmetic might give an infinity, and that operands
+ * below 2^-112 lose their last parts' bits to bf16's subnormals (2e-6 of the norm at
+ * 2^-116, 4e-5 at 2^-120).  Products of up to 16 rows of fp32 are formed by fp32 FMA
+ * and have neither exception.  SiLU and its slope are good to 2^-21 of themselves in
+ * fp32, GELU's Phi to 2^-20 and u^2 2^-23 of itself.
  *
  *   x        : [B, T, K] dtype `dtype`.
  *   w        : [N, K] dtype.

@@ -13,6 +13,7 @@ namespace gecko {
 namespace {
 
 constexpr int64_t kGridYZ = 65535;
+static_assert(kScanChunk == GECKO_SCAN_CHUNK, "the contract's chunk length");
 
 int check_pointers(std::initializer_list<const void*> required, std::initializer_list<const void*> optional) {
   int i = 0;

@@ -68,3 +68,29 @@ def test_forward_and_input_gradient(L, M, keep_pre, D):
     dx, _, _ = L.linear_backward(torch.zeros(M, n, dtype=x.dtype, device="cuda"), w.T.contiguous(), x,
                                  need=(True, False, False))
     _unbiased(dx, want, CUT)
+
+
+def test_captured_and_at_once(L):
+    """Deep products (in runs of the large tiles, of the cluster tiles, in parts) captured and replayed on new inputs,
+    and on two streams at once, are what a call alone gives, bit for bit."""
+    sizes = [(40_000, 2048, 1536), (50_000, 128, 136), (20_000, 1024, 1024), (90_000, 256, 264)]
+    x, dy = ([_positive(M, n, i) for i, (M, *nk) in enumerate(sizes) for n in (nk[j],)] for j in (1, 0))
+    w = [torch.zeros(N, K, dtype=torch.bfloat16, device="cuda") for _, N, K in sizes]
+    calls = lambda: [L.linear_backward(*a, need=(False, True, False))[1] for a in zip(x, w, dy)]
+    want = calls()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(calls())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls()
+    for t in x:
+        t.mul_(2.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, 2 * b) for a, b in zip(outs, want))
